@@ -6,7 +6,7 @@ fallback: if the library is not built, every call raises.
 
 The functions mirror the C ABI in include/bqg.h (same names):
     qgemv, qgemv_batched, qgemv_argmax, qgemv_batched_argmax (GemvBatch.run(argmax=...)),
-    qgemm_prefill, moe_router_logits, moe_router_topk,
+    qgemm_prefill, quantize_rows_i8, qgemm_i8, moe_router_logits, moe_router_topk,
     moe_workspace_size, moe_forward, moe_forward_noalloc, bqg_status_string, bqg_weight_bytes,
     bqg_device_errors, bqg_selftest_wait_timeout
 """
@@ -23,7 +23,8 @@ __all__ = [
     "MOE_PATH_AUTO", "MOE_PATH_CUDA_CORES", "MOE_PATH_TENSOR_CORES",
     "lib", "library_path", "bqg_status_string", "bqg_weight_bytes", "bqg_device_errors",
     "bqg_selftest_wait_timeout",
-    "qgemv", "qgemv_batched", "GemvBatch", "qgemv_argmax", "ArgmaxState", "qgemm_prefill", "moe_router_logits",
+    "qgemv", "qgemv_batched", "GemvBatch", "qgemv_argmax", "ArgmaxState", "qgemm_prefill", "quantize_rows_i8",
+    "qgemm_i8", "moe_router_logits",
     "moe_router_topk", "MoELayer", "moe_workspace_size", "moe_forward", "moe_forward_noalloc", "ExpertCache",
 ]
 
@@ -32,6 +33,7 @@ ACT_GELU_TANH, ACT_SILU = 1, 2
 MOE_PATH_AUTO, MOE_PATH_CUDA_CORES, MOE_PATH_TENSOR_CORES = 0, 1, 2
 MOE_TC_MIN_TOKENS = 8
 MAX_COLS, MAX_BATCH, MAX_EXPERTS, MAX_TOPK, MAX_MOE_COLS = 15360, 256, 256, 8, 7168
+MAX_I8_COLS = 65536
 DEVERR_TIMEOUT, DEVERR_EXPERT_ID = 0x1, 0x2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -80,6 +82,8 @@ _SIGNATURES = {
     "qgemv_argmax": (_i, [_i, _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp]),
     "qgemv_batched_argmax": (_i, [ctypes.POINTER(GemvDesc), _i, _i, _vp, _vp, _vp, _vp]),
     "qgemm_prefill": (_i, [_i, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "quantize_rows_i8": (_i, [_i, _vp, _sz, _vp, _sz, _vp, _i, _i, _vp]),
+    "qgemm_i8": (_i, [_vp, _sz, _vp, _vp, _sz, _vp, _vp, _i, _vp, _sz, _i, _i, _i, _vp]),
     "moe_router_logits": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp]),
     "moe_router_topk": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
     "moe_workspace_size": (_sz, [ctypes.POINTER(MoELayerC), _i]),
@@ -253,6 +257,95 @@ def qgemm_prefill(fmt: int, W: torch.Tensor, X: torch.Tensor, n: int, k: int,
     if X.numel() != tokens * k or Y.numel() < tokens * n or W.numel() < bqg_weight_bytes(fmt, n, k):
         raise ValueError("tensor shapes do not match")
     _check(lib().qgemm_prefill(fmt, _ptr(W), _ptr(X), _ptr(Y), tokens, n, k, _stream(X)), "qgemm_prefill")
+    return Y
+
+
+# ---------------------------------------------------------------- int8 rows and their product
+_TYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
+
+
+def _need_rows(name: str, t: torch.Tensor, dtypes, align: int) -> int:
+    """Checks a 2-D CUDA tensor whose rows are contiguous; returns its row pitch in elements (the
+    row length rounded up to `align` when there is one row, whose stride says nothing)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        return (cols + align - 1) // align * align
+    pitch = t.stride(0)
+    if pitch < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return pitch
+
+
+def _same_device(t: torch.Tensor, *others) -> None:
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"all tensors must be on one device: {t.device} and {o.device}")
+
+
+def _call_on(t: torch.Tensor, what: str, *args) -> None:
+    """Calls the library function `what` with t's device current, on that device's current stream."""
+    if torch.cuda.current_device() == t.device.index:
+        _check(getattr(lib(), what)(*args, _stream(t)), what)
+    else:
+        with torch.cuda.device(t.device):
+            _check(getattr(lib(), what)(*args, _stream(t)), what)
+
+
+def quantize_rows_i8(X: torch.Tensor, Xq: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
+    """Rows of X (fp32, fp16 or bf16 [rows, k], any row pitch) as int8 with one fp32 scale a row:
+    scale = max|row| / 127, Xq = row / scale to the nearest (ties to even).  Returns (Xq, scale);
+    a new Xq is a view [:, :k] of rows padded to whole 16 bytes, as qgemm_i8 takes it."""
+    ldx = _need_rows("X", X, _TYPES, 1)
+    rows, k = X.shape
+    if Xq is None:
+        Xq = torch.empty(rows, (k + 15) // 16 * 16, dtype=torch.int8, device=X.device)
+        if Xq.shape[1] != k:
+            Xq = Xq[:, :k]
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+    ldq = _need_rows("Xq", Xq, (torch.int8,), 16)
+    _need_cuda("scale", scale, torch.float32)
+    if Xq.shape != X.shape or scale.numel() < rows:
+        raise ValueError(f"Xq must be {rows} x {k} and scale must hold {rows} values")
+    _same_device(X, Xq, scale)
+    _call_on(X, "quantize_rows_i8", _TYPES[X.dtype], X.data_ptr(), ldx, Xq.data_ptr(), ldq, scale.data_ptr(), rows, k)
+    return Xq, scale
+
+
+def qgemm_i8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.Tensor,
+             out_dtype: torch.dtype = torch.float16, bias: Optional[torch.Tensor] = None,
+             Y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[t, n] = sx[t] sw[n] sum_i Xq[t, i] Wq[n, i] (+ bias[n]) for int8 Xq [tokens, k] and
+    Wq [n, k] (row pitches of whole 16 bytes), exact int32 sums; Y in out_dtype (fp32, fp16, bf16),
+    or in Y's own type when Y [tokens, n] (any row pitch) is given."""
+    ldx = _need_rows("Xq", Xq, (torch.int8,), 16)
+    ldw = _need_rows("Wq", Wq, (torch.int8,), 16)
+    tokens, k = Xq.shape
+    n = Wq.shape[0]
+    if Wq.shape[1] != k:
+        raise ValueError(f"Xq has {k} columns and Wq {Wq.shape[1]}")
+    if Y is None:
+        if out_dtype not in _TYPES:
+            raise TypeError(f"out_dtype must be {' or '.join(str(d) for d in _TYPES)}, got {out_dtype}")
+        Y = torch.empty(tokens, n, dtype=out_dtype, device=Xq.device)
+    ldy = _need_rows("Y", Y, _TYPES, 1)
+    _need_cuda("sx", sx, torch.float32)
+    _need_cuda("sw", sw, torch.float32)
+    if bias is not None:
+        _need_cuda("bias", bias, torch.float32)
+    if Y.shape != (tokens, n) or sx.numel() < tokens or sw.numel() < n or (bias is not None and bias.numel() < n):
+        raise ValueError(f"Y must be {tokens} x {n}, sx must hold {tokens} values, sw and bias {n}")
+    _same_device(Xq, sx, Wq, sw, bias, Y)
+    _call_on(Xq, "qgemm_i8", Xq.data_ptr(), ldx, sx.data_ptr(), Wq.data_ptr(), ldw, sw.data_ptr(),
+             0 if bias is None else bias.data_ptr(), _TYPES[Y.dtype], Y.data_ptr(), ldy, tokens, n, k)
     return Y
 
 

@@ -11,6 +11,7 @@
 //   moe_api.cuh      moe_forward: workspace, path choice, launches
 //   expert_cache.cuh host-resident experts with a device slot cache
 //   prefill.cuh      tcgen05 prefill-chunk GEMM + qgemm_prefill
+//   i8.cuh           int8 rows and their scaled product (dp4a GEMV, tcgen05 GEMM)
 //   selftest.cuh     failure-detection self-test (a bounded wait that runs out)
 #include "common.cuh"
 #include "host_common.h"
@@ -19,6 +20,7 @@
 #include "moe_api.cuh"
 #include "expert_cache.cuh"
 #include "prefill.cuh"
+#include "i8.cuh"
 #include "selftest.cuh"
 
 extern "C" const char* bqg_status_string(int status) {

@@ -1,0 +1,631 @@
+// Products of 8-bit integers with a scale for each token and each output channel:
+//   q[t, i] = rint(x[t, i] / sx[t]),   sx[t] = max_i |x[t, i]| / 127          (quantize_rows_i8)
+//   Y[t, n] = sx[t] * sw[n] * sum_i q[t, i] * w[n, i]  (+ bias[n])            (qgemm_i8)
+// The sums are exact int32 on every path, so the paths agree bit for bit and results are
+// deterministic; what is rounded is float(sum) (one rounding above 2^24), the two scalings, the
+// bias and the store, in this order.
+//
+// No page describes this step: the pages' CPU engines hold activations as int8 blocks for their
+// integer dots (Camelid README, "Engine status"); this is the whole-row form that a batch of
+// tokens needs, with weights that are int8 rows.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "host_common.h"
+#include "tcgen05.cuh"
+
+namespace bqg {
+
+// ---------------------------------------------------------------- element types
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
+  static __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
+  static __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint32_t bits(float f) { return __half_as_ushort(__float2half_rn(f)); }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint32_t bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+};
+
+// ---------------------------------------------------------------- rows to int8
+// TPR threads own a row (32: 8 rows per CTA, 256: one row per CTA).  A thread keeps up to
+// kQrChunks chunks of 8 values in registers, so rows of up to TPR * 32 values are read once;
+// longer rows read the rest a second time (from L2).  Bytes bound it: 1 read and 1 write of the
+// row.
+//
+// The rounding is decided exactly: with f = floor(x * (1 / s)) (off by at most one), q is f or
+// f + 1 by the sign of fma(-(f + 1/2), s, x), which is the sign of the exact difference (f + 1/2
+// has at most 9 bits; a fused result is 0 only for an exact tie, since s >= 2^-100 keeps it clear
+// of underflow).  A tie goes to the even integer.  A plain rint(x * (1 / s)) would miss borders:
+// bf16 rows meet exact ties often.
+constexpr int kQrThreads = 256;
+constexpr int kQrChunks = 4;
+constexpr float kQrTinyScale = 7.888609052210118e-31f;  // 2^-100: a row below it is held as zeros
+
+__device__ __forceinline__ int round_quotient(float x, float s, float inv) {
+  const float f = floorf(x * inv);
+  const float d = fmaf(-(f + 0.5f), s, x);
+  const int i = int(f);
+  return i + ((d > 0.f || (d == 0.f && (i & 1))) ? 1 : 0);
+}
+
+template <typename T, int TPR, bool VEC>
+__global__ void __launch_bounds__(kQrThreads) k_quantize_rows(const T* __restrict__ X, long long ldx,
+                                                              int8_t* __restrict__ Q, long long ldq,
+                                                              float* __restrict__ scale, int rows, int k) {
+  constexpr int kRows = kQrThreads / TPR;
+  __shared__ uint32_t wmax[kQrThreads / 32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
+  const long long row = (long long)blockIdx.x * kRows + (TPR == 32 ? threadIdx.x >> 5 : 0);
+  if (TPR == 32 && row >= rows) return;
+  const T* x = X + row * ldx;
+  int8_t* q = Q + row * ldq;
+  const int kmain = min(k, TPR * 8 * kQrChunks);
+
+  auto load = [&](int i0, float (&v)[8]) {  // values i0 .. i0 + 7 (0 past the row's end)
+    if (VEC && i0 + 8 <= k) {
+      Elem<T>::load8(x + i0, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = i0 + j < k ? Elem<T>::load(x + i0 + j) : 0.f;
+    }
+  };
+  // |x| as an unsigned integer keeps the order and puts Inf and NaN above every finite value
+  uint32_t most = 0;
+  auto take = [&](const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  };
+  float keep[kQrChunks][8];
+#pragma unroll
+  for (int c = 0; c < kQrChunks; ++c) {
+    const int i0 = (c * TPR + tid) * 8;
+    if (i0 < kmain) load(i0, keep[c]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) keep[c][j] = 0.f;
+  }
+#pragma unroll
+  for (int c = 0; c < kQrChunks; ++c) take(keep[c]);
+  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) {
+    float v[8];
+    load(i0, v);
+    take(v);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQrThreads / 32; ++w) most = max(most, wmax[w]);
+  }
+  float s = __fdiv_rn(__uint_as_float(most), 127.f);
+  const bool finite = most < 0x7F800000u;
+  if (!finite) s = __uint_as_float(0x7FC00000u);  // the whole row of the product becomes NaN
+  else if (s < kQrTinyScale) s = 0.f;
+  if (tid == 0) scale[row] = s;
+  const bool zero = !(s > 0.f);
+  const float inv = zero ? 0.f : __fdiv_rn(1.f, s);
+
+  auto store = [&](int i0, const float (&v)[8]) {
+    uint32_t w[2] = {0u, 0u};
+    if (!zero) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t(round_quotient(v[j], s, inv)) & 0xFFu) << (8 * (j & 3));
+    }
+    if (i0 + 8 <= k) {
+      *reinterpret_cast<uint2*>(q + i0) = make_uint2(w[0], w[1]);
+    } else {
+      for (int j = 0; j < 8 && i0 + j < k; ++j) q[i0 + j] = int8_t(w[j >> 2] >> (8 * (j & 3)));
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < kQrChunks; ++c) {
+    const int i0 = (c * TPR + tid) * 8;
+    if (i0 < kmain) store(i0, keep[c]);
+  }
+  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) {
+    float v[8];
+    load(i0, v);
+    store(i0, v);
+  }
+}
+
+// ---------------------------------------------------------------- the product: arguments
+struct I8Params {
+  const int8_t* X;
+  const int8_t* W;
+  const float* sx;
+  const float* sw;
+  const float* bias;  // or null
+  void* Y;
+  long long ldx, ldw, ldy;
+  int tokens, n, k;
+  int out;   // BQG_F32, BQG_F16 or BQG_BF16
+  int pair;  // 16-bit outputs: rows of Y are 4-byte aligned, two values per store
+};
+
+__device__ __forceinline__ float i8_value(int sum, float sx, float sw, float bias, bool has_bias) {
+  const float v = float(sum) * sx * sw;
+  return has_bias ? v + bias : v;
+}
+
+__device__ __forceinline__ void i8_store(const I8Params& P, long long t, int n, float v) {
+  const long long at = t * P.ldy + n;
+  if (P.out == BQG_F32) static_cast<float*>(P.Y)[at] = v;
+  else if (P.out == BQG_F16) static_cast<__half*>(P.Y)[at] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(P.Y)[at] = __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------- few tokens: a GEMV per token on dp4a
+// A warp owns kIgRows rows of W and walks k in 512-byte steps: lane l reads 16 bytes of each row
+// (coalesced) and of each token's x (from L1, shared by every warp of the SM); 4 dp4a per 16
+// bytes, row and token.  Bound by the weight stream.
+constexpr int kIgThreads = 256;
+constexpr int kIgRows = 4;
+constexpr int kIgMaxTokens = 8;
+
+__device__ __forceinline__ uint4 load16_tail(const int8_t* p, int bytes) {  // 1..15 bytes, the rest 0
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  for (int i = 0; i < bytes; ++i) w[i >> 2] |= uint32_t(uint8_t(p[i])) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int dp16(const uint4& a, const uint4& b, int c) {
+  c = __dp4a(int(a.x), int(b.x), c);
+  c = __dp4a(int(a.y), int(b.y), c);
+  c = __dp4a(int(a.z), int(b.z), c);
+  return __dp4a(int(a.w), int(b.w), c);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kIgThreads) k_i8_gemv(const __grid_constant__ I8Params P) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const long long warps = (long long)gridDim.x * (kIgThreads / 32);
+  const int full = P.k / 16, tail = P.k % 16;
+  const int groups = (P.n + kIgRows - 1) / kIgRows;
+  for (long long g = (long long)blockIdx.x * (kIgThreads / 32) + (threadIdx.x >> 5); g < groups; g += warps) {
+    const int n0 = int(g) * kIgRows;
+    const int8_t* wrow[kIgRows];
+#pragma unroll
+    for (int r = 0; r < kIgRows; ++r) wrow[r] = P.W + (long long)min(n0 + r, P.n - 1) * P.ldw;
+    int acc[kIgRows][NT];
+#pragma unroll
+    for (int r = 0; r < kIgRows; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[r][t] = 0;
+    auto step = [&](const uint4 (&w)[kIgRows], const uint4& xv, int t) {
+#pragma unroll
+      for (int r = 0; r < kIgRows; ++r) acc[r][t] = dp16(w[r], xv, acc[r][t]);
+    };
+#pragma unroll 2
+    for (int c = lane; c < full; c += 32) {
+      uint4 w[kIgRows];
+#pragma unroll
+      for (int r = 0; r < kIgRows; ++r) w[r] = __ldcs(reinterpret_cast<const uint4*>(wrow[r]) + c);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t < P.tokens) step(w, __ldg(reinterpret_cast<const uint4*>(P.X + t * P.ldx) + c), t);
+    }
+    if (tail > 0 && lane == (full & 31)) {  // the last 1..15 values of each row, byte by byte
+      uint4 w[kIgRows];
+#pragma unroll
+      for (int r = 0; r < kIgRows; ++r) w[r] = load16_tail(wrow[r] + full * 16, tail);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t < P.tokens) step(w, load16_tail(P.X + t * P.ldx + full * 16, tail), t);
+    }
+    __syncwarp();
+    int mine = 0;  // lane r * NT + t holds row r of token t
+#pragma unroll
+    for (int r = 0; r < kIgRows; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int v = __reduce_add_sync(0xffffffffu, acc[r][t]);
+        if (lane == r * NT + t) mine = v;
+      }
+    const int r = lane / NT, t = lane % NT;
+    if (r < kIgRows && t < P.tokens && n0 + r < P.n)
+      i8_store(P, t, n0 + r,
+               i8_value(mine, __ldg(P.sx + t), __ldg(P.sw + n0 + r), P.bias ? __ldg(P.bias + n0 + r) : 0.f,
+                        P.bias != nullptr));
+  }
+}
+
+// ---------------------------------------------------------------- many tokens: tcgen05 kind::i8
+// One tile is 128 output channels (rows of W, the MMA's M side: tensor-memory lanes) x BN tokens
+// (N side: columns).  Lane = channel makes the store of one token's column 32 consecutive values
+// of Y per warp, at any pitch, and lets small token counts take a small N.
+//   warp 0     TMA: per stage 128 k of W (128 rows) and of X (BN rows), 128-byte swizzle; rows and
+//              columns past the tensors read as 0
+//   warp 1     allocates tensor memory, issues 4 MMAs (M 128, N BN, K 32) per stage into one of two
+//              int32 accumulators
+//   warps 2-5  scale, convert and store the other accumulator (one warp per 32 lanes)
+// Persistent: CTA b takes tiles b, b + grid, ...
+constexpr int kItThreads = 192;
+constexpr int kItM = 128;
+constexpr int kItK = 128;
+constexpr int kItRaster = 8;  // token tiles walked together (their X and the W tiles of a wave stay in L2)
+__host__ __device__ constexpr int it_stage_bytes(int bn) { return (kItM + bn) * kItK; }
+__host__ __device__ constexpr int it_stages(int bn) {
+  return (216 * 1024) / it_stage_bytes(bn) < 10 ? (216 * 1024) / it_stage_bytes(bn) : 10;
+}
+__host__ __device__ constexpr size_t it_smem_bytes(int bn) {
+  return 1024 + size_t(it_stages(bn)) * it_stage_bytes(bn) + 2 * 256 * sizeof(float) + 256;
+}
+static_assert(it_smem_bytes(256) <= 227 * 1024 && it_smem_bytes(128) <= 227 * 1024 && it_smem_bytes(16) <= 227 * 1024,
+              "int8 product shared memory");
+
+// kind::i8, A and B signed, int32 sums.
+__host__ __device__ constexpr uint32_t umma_idesc_s8(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+__device__ __forceinline__ void umma_i8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// 16 accumulator columns (tokens t0 .. t0 + 15) of this lane's channel.
+template <typename T>
+__device__ __forceinline__ void it_store16h(const I8Params& P, const uint32_t (&v)[16], const float* sx, int t0, int n,
+                                            float sw, float bias, bool has_bias) {
+  const int lane = threadIdx.x & 31;
+  T* Y = static_cast<T*>(P.Y);
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    const uint32_t a = Elem<T>::bits(i8_value(int(v[c]), sx[c], sw, bias, has_bias));
+    const uint32_t b = Elem<T>::bits(i8_value(int(v[c + 1]), sx[c + 1], sw, bias, has_bias));
+    if (P.pair) {
+      // lanes 2i and 2i + 1 swap a value each: the even lane then holds token c of channels n,
+      // n + 1, the odd lane token c + 1 of channels n - 1, n
+      const bool odd = lane & 1;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+      const int t = t0 + c + (odd ? 1 : 0), m = n - (odd ? 1 : 0);
+      const uint32_t two = odd ? (got | (b << 16)) : (a | (got << 16));
+      if (t < P.tokens) {
+        T* y = Y + (long long)t * P.ldy + m;
+        if (m + 1 < P.n) *reinterpret_cast<uint32_t*>(y) = two;
+        else if (m < P.n) *reinterpret_cast<uint16_t*>(y) = uint16_t(two);
+      }
+    } else if (n < P.n) {
+      if (t0 + c < P.tokens) reinterpret_cast<uint16_t*>(Y)[(long long)(t0 + c) * P.ldy + n] = uint16_t(a);
+      if (t0 + c + 1 < P.tokens) reinterpret_cast<uint16_t*>(Y)[(long long)(t0 + c + 1) * P.ldy + n] = uint16_t(b);
+    }
+  }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kItThreads, 1)
+    k_i8_gemm(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+              const __grid_constant__ I8Params P) {
+  constexpr int kStages = it_stages(BN);
+  constexpr int kABytes = kItM * kItK, kBBytes = BN * kItK;
+  constexpr int kCols = 2 * BN < 32 ? 32 : 2 * BN;  // tensor-memory columns: two accumulators
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* a_ring = smem;
+  uint8_t* b_ring = a_ring + size_t(kStages) * kABytes;
+  float* sx_s = reinterpret_cast<float*>(b_ring + size_t(kStages) * kBBytes);  // [2][256]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sx_s + 2 * 256);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;    // [2]
+  uint64_t* done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  static_assert((2 * kStages + 5) * 8 + 4 <= 256, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 128);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  const int ntn = (P.n + kItM - 1) / kItM, ntt = (P.tokens + BN - 1) / BN;
+  const long long tiles = (long long)ntn * ntt;
+  const int nk = (P.k + kItK - 1) / kItK;
+  // tile i: groups of kItRaster token tiles, token tile fastest inside a group
+  auto place = [&](long long i, int& tn, int& tt) {
+    const long long per = (long long)kItRaster * ntn;
+    const int g = int(i / per);
+    const int w = min(kItRaster, ntt - g * kItRaster);
+    const int r = int(i - g * per);
+    tn = r / w;
+    tt = g * kItRaster + r - tn * w;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      long long s = 0;  // stages issued
+      bool ok = true;
+      for (long long i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+        int tn, tt;
+        place(i, tn, tt);
+        for (int kk = 0; kk < nk; ++kk, ++s) {
+          const int st = int(s % kStages);
+          if (s >= kStages && !mbar_wait(&empty[st], uint32_t(s / kStages - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[st], uint32_t(kABytes + kBBytes));
+          tma_load_2d(a_ring + size_t(st) * kABytes, &tmap_w, kk * kItK, tn * kItM, &full[st]);
+          tma_load_2d(b_ring + size_t(st) * kBBytes, &tmap_x, kk * kItK, tt * BN, &full[st]);
+        }
+      }
+      if (!ok)  // bounded wait for the copies already issued, so none lands after the CTA exits
+        for (long long q = (s > kStages ? s - kStages : 0); q < s; ++q)
+          mbar_wait(&full[q % kStages], uint32_t(q / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = umma_idesc_s8(kItM, BN);
+      long long s = 0;
+      int it = 0;
+      bool ok = true;
+      for (long long i = blockIdx.x; i < tiles && ok; i += gridDim.x, ++it) {
+        const int buf = it & 1;
+        if (it >= 2 && !mbar_wait(&acc_empty[buf], uint32_t(it / 2 - 1) & 1u)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + uint32_t(buf * BN);
+        for (int kk = 0; kk < nk; ++kk, ++s) {
+          const int st = int(s % kStages);
+          if (!mbar_wait(&full[st], uint32_t(s / kStages) & 1u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(a_ring + size_t(st) * kABytes), b = smem_u32(b_ring + size_t(st) * kBBytes);
+#pragma unroll
+          for (int j = 0; j < kItK / 32; ++j)
+            umma_i8(acc, umma_desc_sw128(a + 32 * j), umma_desc_sw128(b + 32 * j), idesc, (kk > 0 || j > 0) ? 1u : 0u);
+          umma_commit(&empty[st]);
+        }
+        if (ok) umma_commit(&acc_full[buf]);
+      }
+      umma_commit(done);  // every MMA issued here has completed before tensor memory is freed
+      mbar_wait(done, 0);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const int et = int(threadIdx.x) - 64;  // 0..127
+    const bool has_bias = P.bias != nullptr;
+    int it = 0;
+    for (long long i = blockIdx.x; i < tiles; i += gridDim.x, ++it) {
+      const int buf = it & 1;
+      int tn, tt;
+      place(i, tn, tt);
+      const int n = tn * kItM + quarter * 32 + lane, t0 = tt * BN;
+      float* sx = sx_s + buf * 256;
+      for (int c = et; c < BN; c += 128) sx[c] = t0 + c < P.tokens ? __ldg(P.sx + t0 + c) : 0.f;
+      const float sw = n < P.n ? __ldg(P.sw + n) : 0.f;
+      const float bias = has_bias && n < P.n ? __ldg(P.bias + n) : 0.f;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (!mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u)) break;
+      tc_fence_after();
+      const uint32_t lane_base = tmem + uint32_t(buf * BN) + (uint32_t(quarter * 32) << 16);
+      const int ncol = min(BN, P.tokens - t0);
+#pragma unroll 1
+      for (int c = 0; c < ncol; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(lane_base + uint32_t(c), v);
+        if (P.out == BQG_F32) {
+          if (n < P.n) {
+            float* y = static_cast<float*>(P.Y) + (long long)(t0 + c) * P.ldy + n;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (t0 + c + j < P.tokens) y[j * P.ldy] = i8_value(int(v[j]), sx[c + j], sw, bias, has_bias);
+          }
+        } else if (P.out == BQG_F16) {
+          it_store16h<__half>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
+        } else {
+          it_store16h<__nv_bfloat16>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[buf]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+inline size_t i8_type_bytes(int type) { return type == BQG_F32 ? 4 : (type == BQG_F16 || type == BQG_BF16) ? 2 : 0; }
+
+template <typename T>
+inline int launch_quantize_rows(const void* X, size_t ldx, int8_t* Q, size_t ldq, float* scale, int rows, int k,
+                                cudaStream_t s) {
+  // 8 values a thread by 16-byte loads where every row starts on 16 bytes; one by one otherwise
+  const bool vec = aligned(X, 16) && ldx * sizeof(T) % 16 == 0;
+  const T* x = static_cast<const T*>(X);
+  const long long lx = (long long)ldx, lq = (long long)ldq;
+  if (k <= 32 * 8 * kQrChunks && rows > 1) {  // a warp per row: no barrier; with one row, all the threads
+    const unsigned grid = unsigned((rows + 7) / 8);
+    return vec ? launch_pdl(k_quantize_rows<T, 32, true>, dim3(grid), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k)
+               : launch_pdl(k_quantize_rows<T, 32, false>, dim3(grid), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k);
+  }
+  return vec ? launch_pdl(k_quantize_rows<T, 256, true>, dim3(unsigned(rows)), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k)
+             : launch_pdl(k_quantize_rows<T, 256, false>, dim3(unsigned(rows)), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k);
+}
+
+inline bool i8_encode(CUtensorMap* m, const int8_t* p, size_t pitch, int rows, int k, int box_rows) {
+  EncodeTiledFn encode = encode_tiled_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(k), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(pitch)};
+  const cuuint32_t box[2] = {cuuint32_t(kItK), cuuint32_t(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline SmemAttrOnce g_i8_attr[5];
+
+template <int BN>
+inline int launch_i8_gemm(const I8Params& P, int dev, const DeviceInfo* info, cudaStream_t s) {
+  CUtensorMap tw, tx;
+  if (!i8_encode(&tw, P.W, size_t(P.ldw), P.n, P.k, kItM) || !i8_encode(&tx, P.X, size_t(P.ldx), P.tokens, P.k, BN))
+    return BQG_ERR_CUDA;
+  constexpr int slot = BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : BN == 128 ? 3 : 4;
+  const int st = g_i8_attr[slot].ensure(dev, k_i8_gemm<BN>, it_smem_bytes(BN));
+  if (st != BQG_OK) return st;
+  const long long tiles = (long long)((P.n + kItM - 1) / kItM) * ((P.tokens + BN - 1) / BN);
+  const int grid = int(tiles < info->sm_count ? tiles : info->sm_count);
+  return launch_pdl(k_i8_gemm<BN>, dim3(unsigned(grid)), dim3(kItThreads), it_smem_bytes(BN), s, tw, tx, P);
+}
+
+// Tokens per tile: the one whose waves of tiles take the least time, a tile's 128-k stage costing
+// the larger of its MMAs (2 BN cycles) and its bytes ((128 + BN) * 128 at ~64 bytes a cycle).
+inline int i8_tile_tokens(int tokens, int n, int sms) {
+  const int ntn = (n + kItM - 1) / kItM;
+  int best = 16;
+  long long best_cost = -1;
+  for (int bn = 16; bn <= 256; bn *= 2) {
+    const long long tiles = (long long)ntn * ((tokens + bn - 1) / bn);
+    const long long waves = (tiles + sms - 1) / sms;
+    const long long stage = 2 * bn > 2 * (kItM + bn) ? 2 * bn : 2 * (kItM + bn);
+    const long long cost = waves * stage;
+    if (best_cost < 0 || cost <= best_cost) {
+      best = bn;
+      best_cost = cost;
+    }
+    if (bn >= tokens) break;
+  }
+  return best;
+}
+
+}  // namespace bqg
+
+extern "C" int quantize_rows_i8(int type, const void* X, size_t ldx, int8_t* Xq, size_t ldq, float* scale, int rows,
+                                int k, void* stream) {
+  using namespace bqg;
+  if (X == nullptr || Xq == nullptr || scale == nullptr || rows < 1 || k < 1) return BQG_ERR_ARG;
+  const size_t size = i8_type_bytes(type);
+  if (size == 0) return BQG_ERR_ARG;
+  if (k > BQG_MAX_I8_COLS) return BQG_ERR_LIMIT;
+  if (ldx < size_t(k) || ldq < size_t(k) || ldq % 16 != 0) return BQG_ERR_SHAPE;
+  if (!aligned(X, size) || !aligned(Xq, 16) || !aligned(scale, 4)) return BQG_ERR_ALIGN;
+  int dev;
+  DeviceInfo* info;
+  const int st = current_device(&dev, &info);
+  if (st != BQG_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (type == BQG_F32) return launch_quantize_rows<float>(X, ldx, Xq, ldq, scale, rows, k, s);
+  if (type == BQG_F16) return launch_quantize_rows<__half>(X, ldx, Xq, ldq, scale, rows, k, s);
+  return launch_quantize_rows<__nv_bfloat16>(X, ldx, Xq, ldq, scale, rows, k, s);
+}
+
+extern "C" int qgemm_i8(const int8_t* Xq, size_t ldx, const float* sx, const int8_t* Wq, size_t ldw, const float* sw,
+                        const float* bias, int out_type, void* Y, size_t ldy, int tokens, int n, int k, void* stream) {
+  using namespace bqg;
+  if (Xq == nullptr || sx == nullptr || Wq == nullptr || sw == nullptr || Y == nullptr || tokens < 1 || n < 1 || k < 1)
+    return BQG_ERR_ARG;
+  const size_t size = i8_type_bytes(out_type);
+  if (size == 0) return BQG_ERR_ARG;
+  if (k > BQG_MAX_I8_COLS) return BQG_ERR_LIMIT;
+  if (ldx < size_t(k) || ldw < size_t(k) || ldy < size_t(n) || ldx % 16 != 0 || ldw % 16 != 0) return BQG_ERR_SHAPE;
+  if (!aligned(Xq, 16) || !aligned(Wq, 16) || !aligned(sx, 4) || !aligned(sw, 4) || !aligned(bias, 4) ||
+      !aligned(Y, size))
+    return BQG_ERR_ALIGN;
+  int dev;
+  DeviceInfo* info;
+  const int st = current_device(&dev, &info);
+  if (st != BQG_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  I8Params P{};
+  P.X = Xq;
+  P.W = Wq;
+  P.sx = sx;
+  P.sw = sw;
+  P.bias = bias;
+  P.Y = Y;
+  P.ldx = (long long)ldx;
+  P.ldw = (long long)ldw;
+  P.ldy = (long long)ldy;
+  P.tokens = tokens;
+  P.n = n;
+  P.k = k;
+  P.out = out_type;
+  P.pair = size == 2 && ldy % 2 == 0 && aligned(Y, 4);
+  if (tokens <= kIgMaxTokens) {
+    const int groups = (n + kIgRows - 1) / kIgRows;
+    const int want = (groups + kIgThreads / 32 - 1) / (kIgThreads / 32);
+    const int most = info->sm_count * 6;
+    const dim3 grid(unsigned(want < most ? want : most));
+    if (tokens == 1) return launch_pdl(k_i8_gemv<1>, grid, dim3(kIgThreads), 0, s, P);
+    if (tokens == 2) return launch_pdl(k_i8_gemv<2>, grid, dim3(kIgThreads), 0, s, P);
+    if (tokens <= 4) return launch_pdl(k_i8_gemv<4>, grid, dim3(kIgThreads), 0, s, P);
+    return launch_pdl(k_i8_gemv<8>, grid, dim3(kIgThreads), 0, s, P);
+  }
+  switch (i8_tile_tokens(tokens, n, info->sm_count)) {
+    case 16: return launch_i8_gemm<16>(P, dev, info, s);
+    case 32: return launch_i8_gemm<32>(P, dev, info, s);
+    case 64: return launch_i8_gemm<64>(P, dev, info, s);
+    case 128: return launch_i8_gemm<128>(P, dev, info, s);
+    default: return launch_i8_gemm<256>(P, dev, info, s);
+  }
+}

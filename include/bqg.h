@@ -73,6 +73,7 @@ enum bqg_status {
 
 enum bqg_fmt { BQG_Q8_0 = 1, BQG_Q4_0 = 2, BQG_I4_ROW = 3, BQG_I2_ROW = 4 };
 enum bqg_act { BQG_ACT_GELU_TANH = 1, BQG_ACT_SILU = 2 };
+enum bqg_type { BQG_F32 = 1, BQG_F16 = 2, BQG_BF16 = 3 }; /* element types of quantize_rows_i8 / qgemm_i8 */
 
 /* How moe_forward runs the experts (bqg_moe_layer.path).  Both compute the same layer.
  *   BQG_MOE_PATH_AUTO          the tensor cores (when the shapes allow it) from
@@ -97,6 +98,7 @@ enum bqg_moe_path { BQG_MOE_PATH_AUTO = 0, BQG_MOE_PATH_CUDA_CORES = 1, BQG_MOE_
 #define BQG_MAX_EXPERTS 256      /* largest n_experts of the router / MoE calls            */
 #define BQG_MAX_TOPK 8           /* largest k of the router / MoE calls                    */
 #define BQG_MAX_MOE_COLS 7168    /* largest hidden / inter / shared_inter of moe_forward   */
+#define BQG_MAX_I8_COLS 65536    /* largest k of quantize_rows_i8 / qgemm_i8               */
 
 /* Device-side error bits, reported by bqg_device_errors(). */
 #define BQG_DEVERR_TIMEOUT 0x1   /* a bounded in-kernel wait gave up (the kernel returned early) */
@@ -184,6 +186,38 @@ BQG_API int qgemv_batched_argmax(const bqg_gemv_desc* descs, int n, int argmax_i
  *   summed in a fixed order, so results are deterministic. */
 BQG_API int qgemm_prefill(int fmt, const void* W, const void* X, void* Y, int tokens, int n, int k,
                   void* stream);
+
+/* ---------------------------------------------------------------- int8 rows and their product
+ * The product of 8-bit integers with a scale for each token and each output channel, for any number
+ * of tokens.  The pages describe no such call (their CPU engines hold activations as int8 blocks
+ * for integer dots; Camelid README, "Engine status").
+ *
+ * quantize_rows_i8: every row of X to int8 with one scale (the tokens of a product, or, called
+ * once, the rows of a weight matrix):
+ *   scale[t] = max_i |X[t, i]| / 127, rounded once to fp32;
+ *   Xq[t, i] = X[t, i] / scale[t] rounded to the nearest integer, an exact tie to the even one (the
+ *   quotient is not rounded first), in [-127, 127].
+ * A row whose scale would be below 2^-100 (a row of zeros among them) gets scale 0 and Xq 0.  A row
+ * that holds an Inf or a NaN gets scale NaN and Xq 0, so that its row of the product is NaN.
+ *   type   BQG_F32, BQG_F16 or BQG_BF16: the elements of X.
+ *   X      device [rows x k], row t at X + t * ldx elements (ldx >= k), aligned to its element.
+ *   Xq     device int8, row t at Xq + t * ldq (ldq >= k, a multiple of 16), 16-byte aligned; the
+ *          ldq - k bytes behind a row are left as they are.   scale  device fp32 [rows].
+ *   rows >= 1.   1 <= k <= BQG_MAX_I8_COLS.
+ *
+ * qgemm_i8: Y[t, n] = sx[t] * sw[n] * sum_i Xq[t, i] * Wq[n, i] (+ bias[n]).  The sums are exact in
+ * int32 (any int8 values); the scalings run in fp32, Y is rounded once.  Deterministic.
+ *   Xq     device int8, row t at Xq + t * ldx.   sx  device fp32 [tokens].
+ *   Wq     device int8, row n at Wq + n * ldw.   sw  device fp32 [n].   bias  device fp32 [n] or NULL.
+ *          ldx, ldw >= k, multiples of 16; Xq and Wq 16-byte aligned; the bytes behind a row's k
+ *          values are not used.
+ *   Y      device, out_type (BQG_F32, BQG_F16, BQG_BF16), row t at Y + t * ldy elements (ldy >= n),
+ *          aligned to its element; must not overlap the inputs.
+ *   tokens, n >= 1.   1 <= k <= BQG_MAX_I8_COLS. */
+BQG_API int quantize_rows_i8(int type, const void* X, size_t ldx, int8_t* Xq, size_t ldq, float* scale, int rows, int k,
+                             void* stream);
+BQG_API int qgemm_i8(const int8_t* Xq, size_t ldx, const float* sx, const int8_t* Wq, size_t ldw, const float* sw,
+                     const float* bias, int out_type, void* Y, size_t ldy, int tokens, int n, int k, void* stream);
 
 /* ---------------------------------------------------------------- a5: router logits
  * moe_router_logits: logits[t, e] = sum_h R[e, h] x[t, h] in fp32.
