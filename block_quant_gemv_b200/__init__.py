@@ -7,7 +7,7 @@ fallback: if the library is not built, every call raises.
 The functions mirror the C ABI in include/bqg.h (same names):
     qgemv, qgemv_batched, qgemv_argmax, qgemv_batched_argmax (GemvBatch.run(argmax=...)),
     qgemm_prefill, quantize_rows_i8, qgemm_i8, moe_router_logits, moe_router_topk,
-    moe_workspace_size, moe_forward, moe_forward_noalloc, bqg_status_string, bqg_weight_bytes,
+    moe_workspace_size, moe_forward, moe_forward_noalloc, moe_layer_workspace_size, moe_layer, bqg_status_string, bqg_weight_bytes,
     bqg_device_errors, bqg_selftest_wait_timeout
 """
 from __future__ import annotations
@@ -25,7 +25,8 @@ __all__ = [
     "bqg_selftest_wait_timeout",
     "qgemv", "qgemv_batched", "GemvBatch", "qgemv_argmax", "ArgmaxState", "qgemm_prefill", "quantize_rows_i8",
     "qgemm_i8", "moe_router_logits",
-    "moe_router_topk", "MoELayer", "moe_workspace_size", "moe_forward", "moe_forward_noalloc", "ExpertCache",
+    "moe_router_topk", "MoELayer", "moe_workspace_size", "moe_forward", "moe_forward_noalloc",
+    "moe_layer_workspace_size", "moe_layer_workspace", "moe_layer", "ExpertCache",
 ]
 
 Q8_0, Q4_0, I4_ROW, I2_ROW = 1, 2, 3, 4
@@ -33,7 +34,7 @@ ACT_GELU_TANH, ACT_SILU = 1, 2
 MOE_PATH_AUTO, MOE_PATH_CUDA_CORES, MOE_PATH_TENSOR_CORES = 0, 1, 2
 MOE_TC_MIN_TOKENS = 8
 MAX_COLS, MAX_BATCH, MAX_EXPERTS, MAX_TOPK, MAX_MOE_COLS = 15360, 256, 256, 8, 7168
-MAX_I8_COLS = 65536
+MAX_I8_COLS, MOE_LAYER_MAX_TOKENS, MOE_LAYER_STATE_BYTES = 65536, 8, 512
 DEVERR_TIMEOUT, DEVERR_EXPERT_ID = 0x1, 0x2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -89,6 +90,8 @@ _SIGNATURES = {
     "moe_workspace_size": (_sz, [ctypes.POINTER(MoELayerC), _i]),
     "moe_forward": (_i, [ctypes.POINTER(MoELayerC), _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
     "moe_forward_noalloc": (_i, [ctypes.POINTER(MoELayerC), _vp, _vp, _vp, _vp, _i, _vp]),
+    "moe_layer_workspace_size": (_sz, [ctypes.POINTER(MoELayerC), _i]),
+    "moe_layer": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
     "bqg_selftest_wait_timeout": (_i, [_vp]),
     "bqg_expert_cache_create": (_i, [ctypes.POINTER(ExpertCacheDesc), ctypes.POINTER(_vp)]),
     "bqg_expert_cache_destroy": (None, [_vp]),
@@ -264,59 +267,67 @@ def qgemm_prefill(fmt: int, W: torch.Tensor, X: torch.Tensor, n: int, k: int,
 _TYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
 
 
-def _need_rows(name: str, t: torch.Tensor, dtypes, align: int) -> int:
-    """Checks a 2-D CUDA tensor whose rows are contiguous; returns its row pitch in elements (the
-    row length rounded up to `align` when there is one row, whose stride says nothing)."""
+def _row_pitch(name: str, t: torch.Tensor, dtypes, align: int) -> int:
+    """The row pitch in elements of a 2-D CUDA tensor with contiguous rows (the row length rounded
+    up to `align` when there is one row, whose stride says nothing).  These calls take a few
+    microseconds on the device, so the checks are kept to a few of the host's."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
+    pitch, step = t.stride()
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
     if rows <= 1:
         return (cols + align - 1) // align * align
-    pitch = t.stride(0)
     if pitch < cols:
         raise ValueError(f"the rows of {name} overlap")
     return pitch
 
 
-def _same_device(t: torch.Tensor, *others) -> None:
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"all tensors must be on one device: {t.device} and {o.device}")
+def _vector(name: str, t: torch.Tensor, n: int) -> int:
+    """The address of a contiguous fp32 CUDA tensor of at least n values."""
+    _need_cuda(name, t, torch.float32)
+    if t.numel() < n:
+        raise ValueError(f"{name} must hold {n} values")
+    return t.data_ptr()
 
 
-def _call_on(t: torch.Tensor, what: str, *args) -> None:
-    """Calls the library function `what` with t's device current, on that device's current stream."""
-    if torch.cuda.current_device() == t.device.index:
-        _check(getattr(lib(), what)(*args, _stream(t)), what)
+def _call_on(fn, what: str, tensors, *args) -> None:
+    """Calls a library function with the tensors' device current, on that device's current stream."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors must be on one device: {tensors[0].device} and {t.device}")
+    if torch.cuda.current_device() == device:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
-        with torch.cuda.device(t.device):
-            _check(getattr(lib(), what)(*args, _stream(t)), what)
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if status != 0:
+        raise BQGError(status, what)
 
 
 def quantize_rows_i8(X: torch.Tensor, Xq: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
     """Rows of X (fp32, fp16 or bf16 [rows, k], any row pitch) as int8 with one fp32 scale a row:
     scale = max|row| / 127, Xq = row / scale to the nearest (ties to even).  Returns (Xq, scale);
     a new Xq is a view [:, :k] of rows padded to whole 16 bytes, as qgemm_i8 takes it."""
-    ldx = _need_rows("X", X, _TYPES, 1)
+    ldx = _row_pitch("X", X, _TYPES, 1)
     rows, k = X.shape
     if Xq is None:
         Xq = torch.empty(rows, (k + 15) // 16 * 16, dtype=torch.int8, device=X.device)
-        if Xq.shape[1] != k:
+        if k % 16:
             Xq = Xq[:, :k]
+    elif Xq.shape != X.shape:
+        raise ValueError(f"Xq must be {rows} x {k}")
     if scale is None:
         scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-    ldq = _need_rows("Xq", Xq, (torch.int8,), 16)
-    _need_cuda("scale", scale, torch.float32)
-    if Xq.shape != X.shape or scale.numel() < rows:
-        raise ValueError(f"Xq must be {rows} x {k} and scale must hold {rows} values")
-    _same_device(X, Xq, scale)
-    _call_on(X, "quantize_rows_i8", _TYPES[X.dtype], X.data_ptr(), ldx, Xq.data_ptr(), ldq, scale.data_ptr(), rows, k)
+    ldq = _row_pitch("Xq", Xq, (torch.int8,), 16)
+    _call_on(lib().quantize_rows_i8, "quantize_rows_i8", (X, Xq, scale), _TYPES[X.dtype], X.data_ptr(), ldx,
+             Xq.data_ptr(), ldq, _vector("scale", scale, rows), rows, k)
     return Xq, scale
 
 
@@ -326,26 +337,24 @@ def qgemm_i8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.Ten
     """Y[t, n] = sx[t] sw[n] sum_i Xq[t, i] Wq[n, i] (+ bias[n]) for int8 Xq [tokens, k] and
     Wq [n, k] (row pitches of whole 16 bytes), exact int32 sums; Y in out_dtype (fp32, fp16, bf16),
     or in Y's own type when Y [tokens, n] (any row pitch) is given."""
-    ldx = _need_rows("Xq", Xq, (torch.int8,), 16)
-    ldw = _need_rows("Wq", Wq, (torch.int8,), 16)
+    ldx = _row_pitch("Xq", Xq, (torch.int8,), 16)
+    ldw = _row_pitch("Wq", Wq, (torch.int8,), 16)
     tokens, k = Xq.shape
-    n = Wq.shape[0]
-    if Wq.shape[1] != k:
-        raise ValueError(f"Xq has {k} columns and Wq {Wq.shape[1]}")
+    n, kw = Wq.shape
+    if kw != k:
+        raise ValueError(f"Xq has {k} columns and Wq {kw}")
     if Y is None:
         if out_dtype not in _TYPES:
             raise TypeError(f"out_dtype must be {' or '.join(str(d) for d in _TYPES)}, got {out_dtype}")
         Y = torch.empty(tokens, n, dtype=out_dtype, device=Xq.device)
-    ldy = _need_rows("Y", Y, _TYPES, 1)
-    _need_cuda("sx", sx, torch.float32)
-    _need_cuda("sw", sw, torch.float32)
-    if bias is not None:
-        _need_cuda("bias", bias, torch.float32)
-    if Y.shape != (tokens, n) or sx.numel() < tokens or sw.numel() < n or (bias is not None and bias.numel() < n):
-        raise ValueError(f"Y must be {tokens} x {n}, sx must hold {tokens} values, sw and bias {n}")
-    _same_device(Xq, sx, Wq, sw, bias, Y)
-    _call_on(Xq, "qgemm_i8", Xq.data_ptr(), ldx, sx.data_ptr(), Wq.data_ptr(), ldw, sw.data_ptr(),
-             0 if bias is None else bias.data_ptr(), _TYPES[Y.dtype], Y.data_ptr(), ldy, tokens, n, k)
+        ldy = n
+    else:
+        ldy = _row_pitch("Y", Y, _TYPES, 1)
+        if Y.shape != (tokens, n):
+            raise ValueError(f"Y must be {tokens} x {n}")
+    _call_on(lib().qgemm_i8, "qgemm_i8", (Xq, sx, Wq, sw, bias, Y), Xq.data_ptr(), ldx, _vector("sx", sx, tokens),
+             Wq.data_ptr(), ldw, _vector("sw", sw, n), 0 if bias is None else _vector("bias", bias, n),
+             _TYPES[Y.dtype], Y.data_ptr(), ldy, tokens, n, k)
     return Y
 
 
@@ -490,6 +499,54 @@ def moe_forward_noalloc(layer: MoELayer, x: torch.Tensor, idx: torch.Tensor, w: 
     _check(lib().moe_forward_noalloc(ctypes.byref(layer.c), _ptr(x), _ptr(idx), _ptr(w), _ptr(y), tokens, _stream(x)),
            "moe_forward_noalloc")
     return y
+
+
+# ---------------------------------------------------------------- a whole MoE layer for a few tokens
+def moe_layer_workspace_size(layer: MoELayer, tokens: int) -> int:
+    return int(lib().moe_layer_workspace_size(ctypes.byref(layer.c), tokens))
+
+
+def moe_layer_workspace(layer: MoELayer, tokens: int, device="cuda") -> torch.Tensor:
+    """A workspace of moe_layer for calls of `tokens` tokens, its barrier words zeroed.  Every call
+    leaves them zero; calls that share a workspace must be ordered."""
+    need = moe_layer_workspace_size(layer, tokens)
+    if need == 0:
+        raise ValueError(f"not a valid layer, or tokens not in 1..{MOE_LAYER_MAX_TOKENS}")
+    return torch.zeros(need, dtype=torch.uint8, device=device)
+
+
+def moe_layer(layer: MoELayer, R: torch.Tensor, x: torch.Tensor, y: Optional[torch.Tensor] = None,
+              idx: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None):
+    """The whole layer for 1 to MOE_LAYER_MAX_TOKENS tokens in one kernel: router logits R x, top-k,
+    renormalised softmax weights, the chosen experts and the shared expert.  x is fp32 [tokens,
+    hidden], R fp32 [n_experts, hidden].  Returns (y, idx, w).  Keep a workspace from
+    moe_layer_workspace(); without one each call makes and zeroes its own."""
+    _need_cuda("x", x, torch.float32)
+    _need_cuda("R", R, torch.float32)
+    hidden, k = layer.hidden, layer.top_k
+    tokens = x.numel() // hidden
+    if tokens < 1 or x.numel() != tokens * hidden:
+        raise ValueError(f"x must hold whole tokens of hidden = {hidden} values")
+    if R.numel() != layer.n_experts * hidden:
+        raise ValueError(f"R must be {layer.n_experts} x {hidden}")
+    if y is None:
+        y = torch.empty(tokens, hidden, dtype=torch.float32, device=x.device)
+    if idx is None:
+        idx = torch.empty(tokens, k, dtype=torch.int32, device=x.device)
+    if w is None:
+        w = torch.empty(tokens, k, dtype=torch.float32, device=x.device)
+    _need_cuda("idx", idx, torch.int32)
+    if idx.numel() < tokens * k:
+        raise ValueError(f"idx must hold tokens x top_k = {tokens} x {k} values")
+    if workspace is None and tokens <= MOE_LAYER_MAX_TOKENS:
+        workspace = moe_layer_workspace(layer, tokens, x.device)
+    if workspace is not None:
+        _need_cuda("workspace", workspace, torch.uint8)
+    _call_on(lib().moe_layer, "moe_layer", (x, R, y, idx, w, workspace, layer.tensors[0]), ctypes.addressof(layer.c),
+             R.data_ptr(), x.data_ptr(), _vector("y", y, tokens * hidden), idx.data_ptr(), _vector("w", w, tokens * k),
+             tokens, 0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+    return y, idx, w
 
 
 # ---------------------------------------------------------------- host-resident experts

@@ -9,6 +9,7 @@
 //   moe.cuh          grouped MoE layer kernels (CUDA cores)
 //   moe_tc.cuh       grouped expert GEMM on tcgen05 (many tokens)
 //   moe_api.cuh      moe_forward: workspace, path choice, launches
+//   moe_layer.cuh    a whole MoE layer for a few tokens in one cooperative kernel
 //   expert_cache.cuh host-resident experts with a device slot cache
 //   prefill.cuh      tcgen05 prefill-chunk GEMM + qgemm_prefill
 //   i8.cuh           int8 rows and their scaled product (dp4a GEMV, tcgen05 GEMM)
@@ -18,6 +19,7 @@
 #include "qgemv_api.cuh"
 #include "router.cuh"
 #include "moe_api.cuh"
+#include "moe_layer.cuh"
 #include "expert_cache.cuh"
 #include "prefill.cuh"
 #include "i8.cuh"

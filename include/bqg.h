@@ -98,6 +98,7 @@ enum bqg_moe_path { BQG_MOE_PATH_AUTO = 0, BQG_MOE_PATH_CUDA_CORES = 1, BQG_MOE_
 #define BQG_MAX_EXPERTS 256      /* largest n_experts of the router / MoE calls            */
 #define BQG_MAX_TOPK 8           /* largest k of the router / MoE calls                    */
 #define BQG_MAX_MOE_COLS 7168    /* largest hidden / inter / shared_inter of moe_forward   */
+#define BQG_MOE_LAYER_MAX_TOKENS 8 /* largest token count of moe_layer                      */
 #define BQG_MAX_I8_COLS 65536    /* largest k of quantize_rows_i8 / qgemm_i8               */
 
 /* Device-side error bits, reported by bqg_device_errors(). */
@@ -293,6 +294,32 @@ BQG_API size_t moe_workspace_size(const bqg_moe_layer* L, int tokens);
  *   An expert id outside [0, n_experts) is skipped and sets BQG_DEVERR_EXPERT_ID. */
 BQG_API int moe_forward(const bqg_moe_layer* L, const float* x, const int32_t* idx, const float* w,
                 float* y, int tokens, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- a whole MoE layer for a few tokens
+ * moe_layer: router logits, softmax, top-k, renormalised weights and moe_forward's sum, for 1 to
+ * BQG_MOE_LAYER_MAX_TOKENS tokens, in one kernel (a decode step of one or a few sequences, where
+ * the seven launches of the separate calls cost more than the bytes):
+ *   l = R x[t];  idx[t] = the top_k experts with the largest l in descending order, an exact tie
+ *   going to the lower index;  w[t] = softmax(l) over all experts, renormalised over the chosen;
+ *   y[t] = sum_{j<k} w[t, j] * FFN_{idx[t, j]}(x[t]) (+ shared FFN(x[t])), in slot order.
+ *   Source: TurboFieldfare wiki, "메모리·전문가 스트리밍" (router, top-8 of 128, shared branch);
+ *   Camelid README, "Gemma 4" (captured decode graph).
+ *   L          HOST pointer to the layer description, as for moe_forward; `path` is not used.
+ *   R          device fp32 [n_experts x hidden], 16-byte aligned.
+ *   x          device fp32 [tokens x hidden], 16-byte aligned, finite; y must not overlap it.
+ *   y          device fp32 [tokens x hidden].
+ *   idx, w     device int32 / fp32 [tokens x top_k]: the routing, or both NULL.
+ *   workspace  device, >= moe_layer_workspace_size(L, tokens) bytes, 256-byte aligned.  Zero its
+ *              first BQG_MOE_LAYER_STATE_BYTES once before the first call (cudaMemset); every call leaves
+ *              them zero again, also one that set BQG_DEVERR_TIMEOUT.  The rest is scratch.  Calls
+ *              that share a workspace must be ordered (one stream, or graphs replayed in order).
+ *   x and h are held as 24-bit fixed point per 32 values (|v - s V| <= about 2^-23 max|v|), so y is
+ *   as exact as fp32 sums are; logits and weights are fp32.  Deterministic.  The kernel is a
+ *   cooperative launch of one CTA per SM: it starts when every SM can take its CTA. */
+#define BQG_MOE_LAYER_STATE_BYTES 512
+BQG_API size_t moe_layer_workspace_size(const bqg_moe_layer* L, int tokens);
+BQG_API int moe_layer(const bqg_moe_layer* L, const float* R, const float* x, float* y, int32_t* idx, float* w,
+                      int tokens, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- host-resident experts, device slot cache
  * An expert cache keeps a layer's routed experts in HOST memory (pinned, for asynchronous copies)
