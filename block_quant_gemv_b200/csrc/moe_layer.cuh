@@ -17,7 +17,15 @@
 //      experts stays in the CTA: y is written once, in slot order, with no further barrier.
 // One producer thread streams all the CTA's weights of both phases through one ring of bulk copies
 // and runs ahead of the barriers: the shared expert's rows load during phase 0, the down rows
-// during phase 1 and barrier 2.  Items (a few rows of one matrix) are claimed by single warps.
+// during phase 1 and barrier 2.
+//
+// Work split.  Every CTA takes its share of every touched expert's features (and of the output
+// rows), so that an expert with several tokens costs all CTAs alike.  A row's units of 32 values go
+// to lanes, 32 units ("a slice") to a warp: the warp holds its slice of x in registers while it
+// walks the rows of an item (a few whole rows of one matrix), and leaves one partial sum per row
+// and slice; the slices are added in order afterwards.  Reading x again for every two rows
+// instead, as a warp per whole row would, moves three times the weights' bytes through shared
+// memory (256-expert int4 layer, one token: 121 us).
 //
 // Precision: x and h are 24-bit fixed point per 32 values (three byte planes), so block sums are
 // exact int32 dot products (dp4a) and the only approximation is |x - s X| <= about 2^-23 max|x|.
@@ -33,13 +41,14 @@
 
 namespace bqg {
 
+constexpr int kMlGrid = 148;                       // CTAs: one per SM of a B200
 constexpr int kMlMaxTokens = BQG_MOE_LAYER_MAX_TOKENS;
 constexpr int kMlMaxPairs = kMlMaxTokens * BQG_MAX_TOPK;
 constexpr int kMlWarps = 16;                       // consumer warps
 constexpr int kMlConsumers = 32 * kMlWarps;
 constexpr int kMlThreads = kMlConsumers + 64;      // + producer warp + router warp
 constexpr int kMlMaxSlots = 32;
-constexpr int kMlMaxLogits = 4;                    // experts per CTA in phase 0
+constexpr int kMlArrivals = 8;                     // per slot and turn; a row has up to 7 slices
 constexpr int kMlRecBytes = 112;                   // one unit of 32 values: 3 planes of 32 bytes, scale, pad
 constexpr int kMlUnitMax = 8388600;                // of 2^23 - 1: x * inv rounds up by less than 4
 constexpr int kMlBar = 32;                         // words between barrier counters
@@ -152,11 +161,6 @@ struct MlSum {
 __host__ __device__ constexpr int ml_unit_bytes(int fmt) {
   return fmt == BQG_Q8_0 ? 34 : fmt == BQG_Q4_0 ? 18 : fmt == BQG_I4_ROW ? 16 : 8;
 }
-// The scale of a plane sum: what the in-place byte forms multiply by.
-__host__ __device__ constexpr float ml_factor(int fmt) {
-  return fmt == BQG_Q8_0 ? 1.f : fmt == BQG_I2_ROW ? 1.f / 64.f : 1.f / 16.f;
-}
-
 // The unit at shared-memory byte address u, times X (row scales of int4 / int2 excluded).
 template <int FMT>
 __device__ __forceinline__ float ml_dot(uint32_t u, const MlX& X) {
@@ -200,6 +204,13 @@ __device__ __forceinline__ float ml_dot(uint32_t u, const MlX& X) {
   }
 }
 
+// What a row's plane sums are multiplied by: the byte form's factor and the row scale, if any.
+__device__ __forceinline__ float ml_scale(int fmt, const uint8_t* scales, int row) {
+  if (fmt == BQG_Q8_0) return 1.f;
+  if (fmt == BQG_Q4_0) return 1.f / 16.f;
+  return __ldg(reinterpret_cast<const float*>(scales) + row) * (fmt == BQG_I2_ROW ? 1.f / 64.f : 1.f / 16.f);
+}
+
 // Sums of four values over the warp: every lane gets the total of v[lane & 3].
 __device__ __forceinline__ float ml_reduce4(const float (&v)[4]) {
   const int lane = threadIdx.x & 31;
@@ -224,6 +235,8 @@ struct MlFam {           // matrices of the routed experts (0) or of the shared 
   int off1, off2;        // byte offset of the fp32 row scales (int4, int2) of gate / up, down
   int nf, nr;            // features per item of phase 1 (a gate and an up row each), rows per item of phase 2
   int second;            // phase 1: slot offset of the up rows
+  int share;             // most features of an expert that one CTA has
+  int slices;            // of a row of down
   int x_order;           // which of the two x record sets it reads
 };
 
@@ -235,32 +248,38 @@ struct MlParams {
   int32_t* idx;          // or null
   float* w;
   int tokens, n_experts, top_k, hidden, act, has_shared;
+  int slices;            // of a row of gate / up
   // workspace
   uint32_t* bar;         // barrier counters, one per 128 bytes, zero between calls
   float* logits;         // [tokens][n_experts]
   float* h[2];           // [pairs][inter], [tokens][shared inter]
   uint8_t* xrec[2];      // global x records (when they do not fit shared memory)
   uint8_t* hrec[2];
+  float* sums;           // global partial sums of every CTA (when they do not fit shared memory)
   int x_sets;            // 1 or 2 byte orders of x
   int set_order[2];
   int x_smem, h_smem;    // the records are in shared memory
   // shared memory layout
-  int slots, slot_bytes, rec_off, part_off, rows_cta;
+  int slots, slot_bytes, rec_off, sum_off, rows_cta;
+  int sums_smem;
+  int sums_cta;          // partial sums of a CTA (floats)
 };
 
 struct MlShared {
   uint64_t full[kMlMaxSlots], empty[kMlMaxSlots];
   uint64_t topk_ready, list_ready;
   int4 desc[kMlMaxSlots][2];
-  int next[2];
+  int seq[kMlMaxSlots];  // the item in the slot
+  int next;
   int abort;
-  int n_active, n_shared1, n1, n2;
+  int n_active, n_shared1, n1, tasks2;
   float red[kMlWarps][kMlMaxTokens];
   int sel_e[kMlMaxPairs];
   float sel_w[kMlMaxPairs];
   int act_e[kMlMaxPairs];
   uint32_t act_mask[kMlMaxPairs][2];  // the pairs of a touched expert
   int first[kMlMaxPairs];
+  int pair_a[kMlMaxPairs];            // a pair's expert in act_e
 };
 
 // ---------------------------------------------------------------- grid barriers
@@ -283,17 +302,14 @@ __device__ __forceinline__ bool ml_wait(uint32_t* c, uint32_t n) {
 __device__ __forceinline__ void ml_consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMlConsumers) : "memory"); }
 
 // ---------------------------------------------------------------- work split
-__device__ __forceinline__ int ml_share(long long n, int b) { return int(n * b / gridDim.x); }
+__device__ __forceinline__ int ml_share(int n, int b) { return int((long long)n * b / gridDim.x); }
 __device__ __forceinline__ int ml_div_up(int a, int b) { return (a + b - 1) / b; }
-// Items of the flattened routed features [f0, f1): cut at expert boundaries and every nf features.
-__device__ __forceinline__ int ml_count1(int f0, int f1, int inter, int nf) {
-  int n = 0;
-  for (int f = f0; f < f1;) {
-    const int end = min(f1, (f / inter + 1) * inter);
-    n += ml_div_up(end - f, nf);
-    f = end;
-  }
-  return n;
+// Features [f0, f1) of the a-th touched expert that this CTA has.  The experts' shares are turned
+// against one another, so that the CTAs with the larger ones differ.
+__device__ __forceinline__ void ml_features(int inter, int a, int& f0, int& f1) {
+  const int b = int((blockIdx.x + 61u * unsigned(a)) % gridDim.x);
+  f0 = ml_share(inter, b);
+  f1 = ml_share(inter, b + 1);
 }
 
 // ---------------------------------------------------------------- selection of the experts
@@ -362,6 +378,7 @@ __device__ __forceinline__ void ml_list(MlShared& S, int pairs) {
     int rank = 0;
     for (int q = 0; q < pairs; ++q) rank += S.first[q] && S.sel_e[q] < e;
     S.act_e[rank] = e;
+    S.pair_a[p] = rank;
     atomicOr(&S.act_mask[rank][p >> 5], 1u << (p & 31));
   }
   if (lane == 0) S.n_active = distinct;
@@ -369,19 +386,20 @@ __device__ __forceinline__ void ml_list(MlShared& S, int pairs) {
 }
 
 // ---------------------------------------------------------------- items
-// Phase 1: nf features of one expert, the gate rows at `g`, the up rows at `u` (shared-memory
-// addresses); h of every token of the expert.
+// Slice j of an item for every token of its expert.  Phase 1: n gate rows at shared-memory address
+// `at` and n up rows at `at + up` (row pitch rb), sums [pair][feature][gate, up][slice]; phase 2
+// (up = 0): n rows, sums [pair][row][slice].  X: the slice's x, and `held` the record that it was
+// loaded from (a warp's next item often takes the same one).  Rows are taken four at a time, the
+// last again where there are fewer: one copy of the loop body per format, since the warps of an SM
+// run it out of step and share its instruction cache.
 template <int FMT>
-__device__ __forceinline__ void ml_item1(const MlParams& P, const MlFam& F, MlShared& S, int fam, int a, int f0, int nf,
-                                         uint32_t g, uint32_t u, const uint8_t* xrec) {
+__device__ __forceinline__ void ml_item(uint32_t at, uint32_t up, int rb, int n, int units, int slices, int j,
+                                        uint32_t m0, uint32_t m1, int per_token, const uint8_t* recs, float* sums,
+                                        int pair_step, MlX& X, const uint8_t*& held) {
   const int lane = threadIdx.x & 31;
-  const int units = P.hidden / 32;
-  const int e = fam ? 0 : S.act_e[a];
-  uint32_t m0 = fam ? (1u << P.tokens) - 1u : S.act_mask[a][0], m1 = fam ? 0u : S.act_mask[a][1];
-  const float* gs = reinterpret_cast<const float*>(F.gate + (long long)e * F.gate_stride + F.off1) + f0;
-  const float* us = reinterpret_cast<const float*>(F.up + (long long)e * F.up_stride + F.off1) + f0;
-  constexpr bool kRowScale = FMT == BQG_I4_ROW || FMT == BQG_I2_ROW;
-  constexpr int UB = ml_unit_bytes(FMT);
+  const int c = min(j * 32 + lane, units - 1);
+  const int rows = up ? 2 * n : n, step = up ? 2 * slices : slices;
+  at += uint32_t(c) * ml_unit_bytes(FMT);
   while (m0 | m1) {
     int p;
     if (m0) {
@@ -391,90 +409,38 @@ __device__ __forceinline__ void ml_item1(const MlParams& P, const MlFam& F, MlSh
       p = 31 + __ffs(m1);
       m1 &= m1 - 1;
     }
-    const int t = fam ? p : p / P.top_k;
-    const uint8_t* rec = xrec + size_t(t) * units * kMlRecBytes;
-    float* hrow = P.h[fam] + size_t(p) * F.inter + f0;
-    for (int f = 0; f < nf; f += 2) {
-      const bool two = f + 1 < nf;
-      float rs = 1.f;  // lane & 3: gate f, up f, gate f + 1, up f + 1
-      if (kRowScale && (two || !(lane & 2))) rs = __ldg(((lane & 1) ? us : gs) + f + ((lane >> 1) & 1));
-      const uint32_t ga = g + uint32_t(f) * F.rb1, ua = u + uint32_t(f) * F.rb1;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int c = lane; c < units; c += 32) {
-        MlX X;
-        ml_load_x(rec + size_t(c) * kMlRecBytes, X);
-        v[0] += ml_dot<FMT>(ga + uint32_t(c) * UB, X);
-        v[1] += ml_dot<FMT>(ua + uint32_t(c) * UB, X);
-        if (two) {
-          v[2] += ml_dot<FMT>(ga + F.rb1 + uint32_t(c) * UB, X);
-          v[3] += ml_dot<FMT>(ua + F.rb1 + uint32_t(c) * UB, X);
-        }
-      }
-      __syncwarp();
-      const float s = ml_reduce4(v) * (rs * ml_factor(FMT));
-      const float other = __shfl_xor_sync(0xffffffffu, s, 1);
-      if (lane == 0 || (lane == 2 && two)) hrow[f + (lane >> 1)] = act_fn(P.act, s) * other;
+    const uint8_t* rec = recs + (size_t(p / per_token) * units + c) * kMlRecBytes;
+    if (rec != held) {
+      ml_load_x(rec, X);
+      if (j * 32 + lane >= units) X.s = 0.f;  // a lane past the row's end: the last unit, times zero
+      held = rec;
     }
-  }
-}
-
-// Phase 2: nr rows of one expert's down matrix at `d`; part[pair][row] (shared memory).
-template <int FMT>
-__device__ __forceinline__ void ml_item2(const MlParams& P, const MlFam& F, MlShared& S, int fam, int a, int r0, int nr,
-                                         uint32_t d, const uint8_t* hrec, float* part, int row_base) {
-  const int lane = threadIdx.x & 31;
-  const int units = F.inter / 32;
-  const int e = fam ? 0 : S.act_e[a];
-  const int pairs = P.tokens * P.top_k;
-  uint32_t m0 = fam ? (1u << P.tokens) - 1u : S.act_mask[a][0], m1 = fam ? 0u : S.act_mask[a][1];
-  const float* ds = reinterpret_cast<const float*>(F.down + (long long)e * F.down_stride + F.off2) + r0;
-  constexpr bool kRowScale = FMT == BQG_I4_ROW || FMT == BQG_I2_ROW;
-  constexpr int UB = ml_unit_bytes(FMT);
-  while (m0 | m1) {
-    int p;
-    if (m0) {
-      p = __ffs(m0) - 1;
-      m0 &= m0 - 1;
-    } else {
-      p = 31 + __ffs(m1);
-      m1 &= m1 - 1;
-    }
-    const uint8_t* rec = hrec + size_t(p) * units * kMlRecBytes;
-    float* out = part + (fam ? pairs + p : p) * P.rows_cta + (r0 - row_base);
-    for (int r = 0; r < nr; r += 4) {
-      const int n = min(4, nr - r);
-      float rs = 1.f;
-      if (kRowScale && (lane & 3) < n) rs = __ldg(ds + r + (lane & 3));
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int c = lane; c < units; c += 32) {
-        MlX X;
-        ml_load_x(rec + size_t(c) * kMlRecBytes, X);
-        const uint32_t at = d + uint32_t(r) * F.rb2 + uint32_t(c) * UB;
-        if (n == 4) {
+    __syncwarp();
+    float* sum = sums + size_t(p) * pair_step + j;
+#pragma unroll 1
+    for (int r = 0; r < rows; r += 4) {
+      float v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += ml_dot<FMT>(at + uint32_t(i) * F.rb2, X);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            if (i < n) v[i] += ml_dot<FMT>(at + uint32_t(i) * F.rb2, X);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int q = min(r + i, rows - 1);
+        v[i] = ml_dot<FMT>(at + (q < n ? uint32_t(q * rb) : up + uint32_t((q - n) * rb)), X);
       }
-      __syncwarp();
-      const float s = ml_reduce4(v) * (rs * ml_factor(FMT));
-      if (lane < n) out[r + lane] = s;
+      const float s = ml_reduce4(v);
+      const int q = r + lane;
+      if (lane < 4 && q < rows) sum[q < n ? q * step : (q - n) * step + slices] = s;
     }
   }
 }
 
 // ---------------------------------------------------------------- the kernel
 __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_constant__ MlParams P) {
-  extern __shared__ __align__(128) uint8_t smem[];  // ring, records, parts
+  extern __shared__ __align__(128) uint8_t smem[];  // ring, records, partial sums
   __shared__ MlShared S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = int(blockIdx.x), G = int(gridDim.x);
   const int pairs = P.tokens * P.top_k;
   uint8_t* rec_s = smem + P.rec_off;
-  float* part = reinterpret_cast<float*>(smem + P.part_off);
+  float* sums = P.sums_smem ? reinterpret_cast<float*>(smem + P.sum_off) : P.sums + size_t(b) * P.sums_cta;
 
   // the CTA's shares
   const int sf0 = P.has_shared ? ml_share(P.fam[1].inter, b) : 0, sf1 = P.has_shared ? ml_share(P.fam[1].inter, b + 1) : 0;
@@ -483,11 +449,12 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
   if (threadIdx.x == 0) {
     for (int i = 0; i < P.slots; ++i) {
       mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], 1);
+      mbar_init(&S.empty[i], kMlArrivals);
+      S.seq[i] = -1;
     }
     mbar_init(&S.topk_ready, uint32_t(P.tokens));
     mbar_init(&S.list_ready, 1);
-    S.next[0] = S.next[1] = 0;
+    S.next = 0;
     S.abort = 0;
     S.n_shared1 = P.has_shared ? ml_div_up(sf1 - sf0, P.fam[1].nf) : 0;
     fence_barrier_init();
@@ -533,7 +500,8 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         o0 = rows_in(at, 0, m0, rb, rows, r0, n, bytes, bar, false);
         if (first) o1 = rows_in(at, F.second, m1, rb, rows, r0, n, bytes, bar, false);
         S.desc[slot][0] = make_int4(type, a, r0, n);
-        S.desc[slot][1] = make_int4(o0, o1, 0, 0);
+        S.desc[slot][1] = make_int4(o0, o1, e, 0);
+        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&S.seq[slot])), "r"(i) : "memory");
         if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
         else mbar_arrive(bar);
         rows_in(at, 0, m0, rb, rows, r0, n, bytes, bar, true);
@@ -545,13 +513,11 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       for (int f = sf0; f < sf1 && ok; f += P.fam[1].nf) ok = put(1, 0, P.fam[1], 0, f, min(P.fam[1].nf, sf1 - f));
       ok = ok && mbar_wait(&S.list_ready, 0) && !*(volatile int*)&S.abort;
       if (ok) {
-        const int na = S.n_active, I = P.fam[0].inter;
-        const int f1 = ml_share((long long)na * I, b + 1);
-        for (int f = ml_share((long long)na * I, b); f < f1 && ok;) {
-          const int a = f / I, in = f - a * I;
-          const int n = min(min(P.fam[0].nf, I - in), f1 - f);
-          ok = put(0, a, P.fam[0], S.act_e[a], in, n);
-          f += n;
+        const int na = S.n_active;
+        for (int a = 0; a < na && ok; ++a) {
+          int f0, f1;
+          ml_features(P.fam[0].inter, a, f0, f1);
+          for (int f = f0; f < f1 && ok; f += P.fam[0].nf) ok = put(0, a, P.fam[0], S.act_e[a], f, min(P.fam[0].nf, f1 - f));
         }
         // phase 2 (types 2 / 3: routed / shared)
         if (P.has_shared)
@@ -579,12 +545,19 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     __syncwarp();
     if (ok) {
       ml_list(S, pairs);
+      const int na = S.n_active;
+      int n1 = 0;
+      for (int a = lane; a < na; a += 32) {
+        int f0, f1;
+        ml_features(P.fam[0].inter, a, f0, f1);
+        n1 += ml_div_up(f1 - f0, P.fam[0].nf);
+      }
+      n1 = __reduce_add_sync(0xffffffffu, n1);
       if (lane == 0) {
-        const int na = S.n_active, I = P.fam[0].inter;
-        S.n1 = S.n_shared1 +
-               ml_count1(ml_share((long long)na * I, b), ml_share((long long)na * I, b + 1), I, P.fam[0].nf);
         const int rows = hr1 - hr0;
-        S.n2 = (P.has_shared ? ml_div_up(rows, P.fam[1].nr) : 0) + na * ml_div_up(rows, P.fam[0].nr);
+        S.n1 = S.n_shared1 + n1;
+        S.tasks2 = (P.has_shared ? ml_div_up(rows, P.fam[1].nr) * P.fam[1].slices : 0) +
+                   na * ml_div_up(rows, P.fam[0].nr) * P.fam[0].slices;
       }
       if (b == 0 && P.idx != nullptr)
         for (int p = lane; p < pairs; p += 32) {
@@ -661,54 +634,111 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     };
     if (!P.x_smem) need_list();  // the records in global memory are complete behind barrier 1
 
-    auto claim = [&](int phase) {
-      int i = 0;
-      if (lane == 0) i = atomicAdd(&S.next[phase], 1);
-      return __shfl_sync(0xffffffffu, i, 0);
-    };
     const uint32_t ring_s = smem_u32(smem);
-    auto run_item = [&](int i) -> bool {
+    MlX X;
+    const uint8_t* held = nullptr;
+    // Slice j of item i.  The item is in its slot once the slot's sequence number says so, and only
+    // then does the parity of `full` tell the item's own phase.
+    auto run_item = [&](int i, int j) -> bool {
       const int slot = i % P.slots;
+      int seq;
+      const unsigned long long t0 = globaltimer_ns();
+      for (;;) {
+        asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(seq) : "r"(smem_u32(&S.seq[slot])) : "memory");
+        if (seq == i) break;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          flag_error(BQG_DEVERR_TIMEOUT);
+          return false;
+        }
+        __nanosleep(40);
+      }
       if (!mbar_wait(&S.full[slot], uint32_t(i / P.slots) & 1u)) return false;
       const int4 d = ld_desc(&S.desc[slot][0]), o = ld_desc(&S.desc[slot][1]);
       const uint32_t at = ring_s + uint32_t(slot) * P.slot_bytes;
       const int fam = d.x & 1;
+      const bool first = d.x < 2;
       const MlFam& F = P.fam[fam];
-      if (d.x < 2) {
+      const int slices = first ? P.slices : F.slices;
+      const uint32_t m0 = fam ? (1u << P.tokens) - 1u : S.act_mask[d.y][0], m1 = fam ? 0u : S.act_mask[d.y][1];
+      const uint8_t* recs;
+      float* out;
+      int pair_step, n_units, per_token;
+      if (first) {
         const int s = F.x_order;
-        const uint8_t* xrec = P.x_smem ? rec_s + size_t(s) * P.tokens * units * kMlRecBytes : P.xrec[s];
-        switch (F.fmt) {
-          case BQG_Q8_0: ml_item1<BQG_Q8_0>(P, F, S, fam, d.y, d.z, d.w, at + o.x, at + o.y, xrec); break;
-          case BQG_Q4_0: ml_item1<BQG_Q4_0>(P, F, S, fam, d.y, d.z, d.w, at + o.x, at + o.y, xrec); break;
-          case BQG_I4_ROW: ml_item1<BQG_I4_ROW>(P, F, S, fam, d.y, d.z, d.w, at + o.x, at + o.y, xrec); break;
-          default: ml_item1<BQG_I2_ROW>(P, F, S, fam, d.y, d.z, d.w, at + o.x, at + o.y, xrec); break;
-        }
+        int f0, f1;
+        ml_features(F.inter, fam ? 0 : d.y, f0, f1);
+        recs = P.x_smem ? rec_s + size_t(s) * P.tokens * units * kMlRecBytes : P.xrec[s];
+        n_units = units;
+        pair_step = F.share * 2 * slices;
+        out = sums + (fam ? size_t(pairs) * P.fam[0].share * 2 * slices : 0) + (d.z - f0) * 2 * slices;
+        per_token = fam ? 1 : P.top_k;
       } else {
-        const size_t shared_at = size_t(pairs) * (P.fam[0].inter / 32) * kMlRecBytes;
-        const uint8_t* hrec = P.h_smem ? rec_s + (fam ? shared_at : 0) : P.hrec[fam];
-        switch (F.fmt) {
-          case BQG_Q8_0: ml_item2<BQG_Q8_0>(P, F, S, fam, d.y, d.z, d.w, at + o.x, hrec, part, hr0); break;
-          case BQG_Q4_0: ml_item2<BQG_Q4_0>(P, F, S, fam, d.y, d.z, d.w, at + o.x, hrec, part, hr0); break;
-          case BQG_I4_ROW: ml_item2<BQG_I4_ROW>(P, F, S, fam, d.y, d.z, d.w, at + o.x, hrec, part, hr0); break;
-          default: ml_item2<BQG_I2_ROW>(P, F, S, fam, d.y, d.z, d.w, at + o.x, hrec, part, hr0); break;
-        }
+        recs = P.h_smem ? rec_s + (fam ? size_t(pairs) * (P.fam[0].inter / 32) * kMlRecBytes : 0) : P.hrec[fam];
+        n_units = F.inter / 32;
+        pair_step = P.rows_cta * slices;
+        out = sums + (fam ? size_t(pairs) * P.rows_cta * P.fam[0].slices : 0) + (d.z - hr0) * slices;
+        per_token = 1;
+      }
+      const uint32_t up = first ? uint32_t(o.y - o.x) : 0u;
+      const int rb = first ? F.rb1 : F.rb2;
+      switch (F.fmt) {
+        case BQG_Q8_0:
+          ml_item<BQG_Q8_0>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
+          break;
+        case BQG_Q4_0:
+          ml_item<BQG_Q4_0>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
+          break;
+        case BQG_I4_ROW:
+          ml_item<BQG_I4_ROW>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
+          break;
+        default:
+          ml_item<BQG_I2_ROW>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.empty[slot]);
+      if (lane == 0)  // the slot is free when all its slices are done
+        asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&S.empty[slot])),
+                     "r"(j == 0 ? kMlArrivals - (slices - 1) : 1)
+                     : "memory");
       return true;
     };
 
-    // At most `slots` warps claim items: claimed items then lie within one turn of the ring, and a
-    // warp can never wait for a slot's phase after next, which the parity could not tell apart.
-    const bool worker = warp < P.slots;
-    // phase 1
-    while (ok && worker) {
-      const int i = claim(0);
-      if (i >= S.n_shared1 && (!need_list() || i >= S.n1)) break;
-      if (!run_item(i)) ok = false;
+    // phase 1: warp = (group, slice); group g takes items g, g + groups, ..., so that a warp stays on
+    // its slice of x
+    {
+      const int groups = kMlWarps / P.slices;
+      if (warp < groups * P.slices) {
+        const int j = warp % P.slices;
+        for (int i = warp / P.slices; ok; i += groups) {
+          if (i >= S.n_shared1 && (!need_list() || i >= S.n1)) break;
+          if (!run_item(i, j)) ok = false;
+        }
+      }
     }
     if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
     need_list();
+    ml_consumers_sync();
+    // h = act(g) u of the CTA's features, the slices added in order
+    if (!*(volatile int*)&S.abort) {
+      const int n0 = pairs * P.fam[0].share, n = n0 + (P.has_shared ? P.tokens * P.fam[1].share : 0);
+      for (int i = tid; i < n; i += kMlConsumers) {
+        const int fam = i >= n0 ? 1 : 0;
+        const MlFam& F = P.fam[fam];
+        const int p = (i - fam * n0) / F.share, f = (i - fam * n0) - p * F.share;
+        int f0, f1;
+        ml_features(F.inter, fam ? 0 : S.pair_a[p], f0, f1);
+        if (f0 + f >= f1) continue;
+        const float* s = sums + size_t(i) * 2 * P.slices;
+        float g = 0.f, u = 0.f;
+        for (int j = 0; j < P.slices; ++j) {
+          g += s[j];
+          u += s[P.slices + j];
+        }
+        const long long e = fam ? 0 : S.sel_e[p];
+        g *= ml_scale(F.fmt, F.gate + e * F.gate_stride + F.off1, f0 + f);
+        u *= ml_scale(F.fmt, F.up + e * F.up_stride + F.off1, f0 + f);
+        P.h[fam][size_t(p) * F.inter + f0 + f] = act_fn(P.act, g) * u;
+      }
+    }
     ml_consumers_sync();
     // grid barrier 2: every h is written
     if (tid == 0) {
@@ -732,22 +762,43 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       }
       ml_consumers_sync();
     }
-    // phase 2
+    // phase 2: a warp claims slices of items
     ok = !*(volatile int*)&S.abort;
-    while (ok && worker) {
-      const int i = claim(1);
-      if (i >= S.n2) break;
-      if (!run_item(S.n1 + i)) ok = false;
+    held = nullptr;
+    {
+      const int rows = hr1 - hr0;
+      const int si = P.has_shared ? ml_div_up(rows, P.fam[1].nr) : 0, st = si * P.fam[1].slices;
+      while (ok) {
+        int t = 0;
+        if (lane == 0) t = atomicAdd(&S.next, 1);
+        t = __shfl_sync(0xffffffffu, t, 0);
+        if (t >= S.tasks2) break;
+        const int fam = t < st ? 1 : 0;
+        const int in = t - (fam ? 0 : st), slices = P.fam[fam].slices;
+        if (!run_item(S.n1 + (fam ? 0 : si) + in / slices, in % slices)) ok = false;
+      }
     }
     if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
     ml_consumers_sync();
     if (!*(volatile int*)&S.abort) {
-      const int rows = hr1 - hr0;
+      const int rows = hr1 - hr0, sl0 = P.fam[0].slices, sl1 = P.fam[1].slices;
       for (int i = tid; i < P.tokens * rows; i += kMlConsumers) {
         const int t = i / rows, r = i - t * rows;
         float acc = 0.f;
-        for (int j = 0; j < P.top_k; ++j) acc = fmaf(S.sel_w[t * P.top_k + j], part[(t * P.top_k + j) * P.rows_cta + r], acc);
-        if (P.has_shared) acc += part[(pairs + t) * P.rows_cta + r];
+        for (int q = 0; q < P.top_k; ++q) {
+          const int p = t * P.top_k + q;
+          const float* s = sums + (size_t(p) * P.rows_cta + r) * sl0;
+          float v = 0.f;
+          for (int j = 0; j < sl0; ++j) v += s[j];
+          v *= ml_scale(P.fam[0].fmt, P.fam[0].down + (long long)S.sel_e[p] * P.fam[0].down_stride + P.fam[0].off2, hr0 + r);
+          acc = fmaf(S.sel_w[p], v, acc);
+        }
+        if (P.has_shared) {
+          const float* s = sums + size_t(pairs) * P.rows_cta * sl0 + (size_t(t) * P.rows_cta + r) * sl1;
+          float v = 0.f;
+          for (int j = 0; j < sl1; ++j) v += s[j];
+          acc += v * ml_scale(P.fam[1].fmt, P.fam[1].down + P.fam[1].off2, hr0 + r);
+        }
         P.y[size_t(t) * P.hidden + hr0 + r] = acc;
       }
     }
@@ -766,14 +817,17 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
 static_assert(4 * kMlBar * sizeof(uint32_t) <= BQG_MOE_LAYER_STATE_BYTES, "barrier counters");
 
 struct MlLayout {
-  size_t bar, logits, h[2], xrec[2], hrec[2], total;
-  int x_sets, set_order[2], x_order[2], x_smem, h_smem;
-  size_t rec_bytes;
+  size_t bar, logits, h[2], xrec[2], hrec[2], sums, total;
+  int x_sets, set_order[2], x_order[2], x_smem, h_smem, sums_smem;
+  size_t rec_bytes, sums_cta;
 };
 constexpr size_t kMlRecCap = 64 * 1024;  // records kept in shared memory (the ring needs the rest)
+constexpr size_t kMlSumCap = 32 * 1024;  // partial sums kept in shared memory
 constexpr size_t kMlSmem = 227 * 1024 - sizeof(MlShared) - 1024;
 
-inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens) {
+inline int ml_slices(int cols) { return (cols / 32 + 31) / 32; }
+
+inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens, int grid) {
   MlLayout o{};
   const bool sh = L->s_gate != nullptr;
   const size_t T = size_t(tokens), pairs = T * L->top_k;
@@ -806,14 +860,22 @@ inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens) {
   }
   if (o.x_smem) o.rec_bytes = xb * o.x_sets;
   if (o.h_smem && hb0 + hb1 > o.rec_bytes) o.rec_bytes = hb0 + hb1;
+  // partial sums of a CTA: the larger of the two phases'
+  auto up = [&](int n) { return size_t((n + grid - 1) / grid); };
+  const size_t s1 = 2 * size_t(ml_slices(L->hidden)) * (pairs * up(L->inter) + (sh ? T * up(L->shared_inter) : 0));
+  const size_t s2 = up(L->hidden) * (pairs * ml_slices(L->inter) + (sh ? T * ml_slices(L->shared_inter) : 0));
+  o.sums_cta = s1 > s2 ? s1 : s2;
+  o.sums_smem = 4 * o.sums_cta <= kMlSumCap;
+  if (!o.sums_smem) o.sums = take(4 * o.sums_cta * grid);
   o.total = off;
   return o;
 }
 
-// Rows per item: about 6.5 KB, so that the ring holds 25 to 30 items and 16 warps find work while
-// the rest load.
+// Rows per item: the CTA's share of an expert in equal pieces of at most about kMlItem bytes, so that
+// a warp's slice of x serves many rows and the ring still holds several items.
+constexpr int kMlItem = 24 * 1024;
 inline MlFam ml_fam(int fmt, int hidden, int inter, const void* gate, const void* up, const void* down, size_t gs,
-                    size_t us, size_t ds, int x_order) {
+                    size_t us, size_t ds, int x_order, int grid) {
   MlFam F{};
   F.gate = static_cast<const uint8_t*>(gate);
   F.up = static_cast<const uint8_t*>(up);
@@ -829,11 +891,15 @@ inline MlFam ml_fam(int fmt, int hidden, int inter, const void* gate, const void
     F.off1 = int((size_t(inter) * F.rb1 + 15) / 16 * 16);
     F.off2 = int((size_t(hidden) * F.rb2 + 15) / 16 * 16);
   }
-  constexpr int kItem = 6656;
-  F.nf = kItem / (2 * F.rb1);
-  F.nf = F.nf < 1 ? 1 : F.nf > 8 ? 8 : F.nf;
-  F.nr = kItem / F.rb2;
-  F.nr = F.nr < 1 ? 1 : F.nr > 32 ? 32 : F.nr >= 4 ? F.nr / 4 * 4 : F.nr;
+  auto pieces = [](int n, long long bytes) {  // n rows of `bytes` in equal pieces
+    const long long most = kMlItem / bytes < 1 ? 1 : kMlItem / bytes;
+    const long long k = (n + most - 1) / most;
+    return int((n + k - 1) / k);
+  };
+  F.share = (inter + grid - 1) / grid;
+  F.nf = pieces(F.share, 2 * F.rb1);
+  F.nr = pieces((hidden + grid - 1) / grid, F.rb2);
+  F.slices = ml_slices(inter);
   F.second = (F.nf * F.rb1 + 32 + 15) / 16 * 16;
   F.x_order = x_order;
   return F;
@@ -849,7 +915,7 @@ inline SmemAttrOnce g_ml_attr;
 
 extern "C" size_t moe_layer_workspace_size(const bqg_moe_layer* L, int tokens) {
   if (bqg::check_layer(L) != BQG_OK || tokens < 1 || tokens > bqg::kMlMaxTokens) return 0;
-  return bqg::ml_layout(L, tokens).total;
+  return bqg::ml_layout(L, tokens, bqg::kMlGrid).total;
 }
 
 extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x, float* y, int32_t* idx, float* w,
@@ -860,20 +926,21 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   if (R == nullptr || x == nullptr || y == nullptr || tokens < 1 || (idx == nullptr) != (w == nullptr)) return BQG_ERR_ARG;
   if (tokens > kMlMaxTokens) return BQG_ERR_LIMIT;
   if (!aligned(R, 16) || !aligned(x, 16) || !aligned(y, 4) || !aligned(idx, 4) || !aligned(w, 4)) return BQG_ERR_ALIGN;
-  const MlLayout lay = ml_layout(L, tokens);
+  const MlLayout lay = ml_layout(L, tokens, kMlGrid);
   if (workspace == nullptr || ws_bytes < lay.total) return BQG_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return BQG_ERR_ALIGN;
   int dev;
   DeviceInfo* info;
   st = current_device(&dev, &info);
   if (st != BQG_OK) return st;
+  if (info->sm_count < kMlGrid) return BQG_ERR_DEVICE;  // part of a GPU: its CTAs could not all be resident
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool sh = L->s_gate != nullptr;
 
   MlParams P{};
   P.fam[0] = ml_fam(L->expert_fmt, L->hidden, L->inter, L->gate, L->up, L->down, L->gate_stride, L->up_stride,
-                    L->down_stride, 0);
-  P.fam[1] = sh ? ml_fam(L->shared_fmt, L->hidden, L->shared_inter, L->s_gate, L->s_up, L->s_down, 0, 0, 0, lay.x_order[1])
+                    L->down_stride, 0, kMlGrid);
+  P.fam[1] = sh ? ml_fam(L->shared_fmt, L->hidden, L->shared_inter, L->s_gate, L->s_up, L->s_down, 0, 0, 0, lay.x_order[1], kMlGrid)
                 : P.fam[0];
   P.R = R;
   P.x = x;
@@ -897,25 +964,26 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   P.x_sets = lay.x_sets;
   P.x_smem = lay.x_smem;
   P.h_smem = lay.h_smem;
-  const int grid = info->sm_count;
-  P.rows_cta = (L->hidden + grid - 1) / grid;
+  P.slices = ml_slices(L->hidden);
+  P.sums = reinterpret_cast<float*>(ws + lay.sums);
+  P.sums_smem = lay.sums_smem;
+  P.sums_cta = int(lay.sums_cta);
+  P.rows_cta = (L->hidden + kMlGrid - 1) / kMlGrid;
   const int s0 = ml_slot(P.fam[0]), s1 = ml_slot(P.fam[1]);
   P.slot_bytes = s0 > s1 ? s0 : s1;
-  const size_t part_bytes = size_t(4) * P.rows_cta * (size_t(tokens) * L->top_k + tokens);
+  const size_t sum_bytes = lay.sums_smem ? (4 * lay.sums_cta + 127) / 128 * 128 : 0;
   const size_t rec_bytes = (lay.rec_bytes + 127) / 128 * 128;
-  const size_t rest = rec_bytes + part_bytes;
-  if (rest + 4 * size_t(P.slot_bytes) > kMlSmem) return BQG_ERR_LIMIT;
-  size_t slots = (kMlSmem - rest) / size_t(P.slot_bytes);
+  size_t slots = (kMlSmem - rec_bytes - sum_bytes) / size_t(P.slot_bytes);
   if (slots > size_t(kMlMaxSlots)) slots = kMlMaxSlots;
   P.slots = int(slots);
   P.rec_off = P.slots * P.slot_bytes;
-  P.part_off = P.rec_off + int(rec_bytes);
-  const size_t smem = size_t(P.part_off) + part_bytes;
+  P.sum_off = P.rec_off + int(rec_bytes);
+  const size_t smem = size_t(P.sum_off) + sum_bytes;
   if ((st = g_ml_attr.ensure(dev, k_moe_layer, kMlSmem)) != BQG_OK) return st;
 
   // cooperative: the CTAs wait for one another, so all of them must be resident
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(grid));
+  cfg.gridDim = dim3(unsigned(kMlGrid));
   cfg.blockDim = dim3(kMlThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
