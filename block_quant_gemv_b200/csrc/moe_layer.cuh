@@ -9,29 +9,34 @@
 //   0  logits of the CTA's experts; x in integer form
 //      -- grid barrier 1 --
 //      every CTA selects the experts of all tokens itself (no second barrier) and lists them
-//   1  gate and up rows of the CTA's share of the features, h = act(g) u
+//   1  gate and up rows of the CTA's items, h = act(g) u
 //      -- grid barrier 2 --
 //      h in integer form (own copy in shared memory when it fits; else shared out over the grid and
 //      grid barrier 3)
 //   2  down: the CTA's share of the output rows, for every touched expert, so that the sum over
 //      experts stays in the CTA: y is written once, in slot order, with no further barrier.
-// One producer thread streams all the CTA's weights of both phases through one ring of bulk copies
+// One producer warp streams all the CTA's weights of both phases through one ring of bulk copies
 // and runs ahead of the barriers: the shared expert's rows load during phase 0, the down rows
 // during phase 1 and barrier 2.
 //
-// Work split.  Every CTA takes its share of every touched expert's features (and of the output
-// rows), so that an expert with several tokens costs all CTAs alike.  A row's units of 32 values go
-// to lanes, 32 units ("a slice") to a warp: the warp holds its slice of x in registers while it
-// walks the rows of an item (a few whole rows of one matrix), and leaves one partial sum per row
-// and slice; the slices are added in order afterwards.  Reading x again for every two rows
-// instead, as a warp per whole row would, moves three times the weights' bytes through shared
-// memory (256-expert int4 layer, one token: 121 us).
+// Products.  A warp multiplies a tile of 16 weight rows by up to 8 columns with the integer MMA of
+// the register file (m16n8k32): the weights become signed bytes in registers on their way from
+// shared memory, so nothing is written back, which operands in tensor memory or shared memory would
+// need, and at 8 columns the rate of the instruction is not the bound (0.49 a clock and SM measured:
+// a GLM-like layer's 302 M weights take 4 us).  The columns are the digits of x: x and h are 24-bit
+// fixed point per row, as three signed byte digits (256 m + l + 65536 h), and columns 4 t .. 4 t + 2
+// hold the middle, low and high digit of the group's token t (two tokens a pass).  All sums of a
+// block (Q8_0, Q4_0) or of the row (int4, int2) are exact integers; the only approximation is
+// |x - s X| <= about 2^-23 max|x|.  Nibble and 2-bit weights are taken as signed bytes in place (a
+// nibble in the high half of its byte is 16 q, a 2-bit code in the top bits 64 q; q - 8 of Q4_0 is
+// the two's-complement nibble u ^ 8): no offset corrections.
+// A dp4a per digit instead was bound by instructions (256-expert int4 layer: 76 us for one token,
+// 403 us for 8).
 //
-// Precision: x and h are 24-bit fixed point per 32 values (three byte planes), so block sums are
-// exact int32 dot products (dp4a) and the only approximation is |x - s X| <= about 2^-23 max|x|.
-// Nibble and 2-bit weights are taken as signed bytes in place (a nibble in the high half of its
-// byte is 16 q, a 2-bit code in the top bits 64 q; q - 8 of Q4_0 is the two's-complement nibble
-// u ^ 8): no offset corrections.
+// Work split.  Phase 1: items of up to 8 features (8 gate rows, the same 8 up rows: one tile) are
+// dealt out over the grid one by one.  Phase 2: the CTA's rows of one expert in tiles of up to 16.
+// An item's k range is cut into parts, one consumer warp each; the last part's warp adds the parts in
+// order.
 #pragma once
 
 #include "common.cuh"
@@ -46,182 +51,228 @@ constexpr int kMlMaxTokens = BQG_MOE_LAYER_MAX_TOKENS;
 constexpr int kMlMaxPairs = kMlMaxTokens * BQG_MAX_TOPK;
 constexpr int kMlWarps = 16;                       // consumer warps
 constexpr int kMlConsumers = 32 * kMlWarps;
-constexpr int kMlThreads = kMlConsumers + 64;      // + producer warp + router warp
-constexpr int kMlMaxSlots = 32;
-constexpr int kMlArrivals = 8;                     // per slot and turn; a row has up to 7 slices
-constexpr int kMlRecBytes = 112;                   // one unit of 32 values: 3 planes of 32 bytes, scale, pad
-constexpr int kMlUnitMax = 8388600;                // of 2^23 - 1: x * inv rounds up by less than 4
+constexpr int kMlHelpers = 3;                      // warps that select the experts and finish h
+constexpr int kMlThreads = kMlConsumers + 32 + 32 * kMlHelpers;  // + producer warp
+constexpr int kMlSlots = 8;                        // items in the ring
+constexpr int kMlDigitMax = 8355700;               // of 127 * 65793: x * inv rounds up by less than 4
 constexpr int kMlBar = 32;                         // words between barrier counters
+constexpr int kMlHmax = 4 * kMlBar;                // the rows' max|h| behind the counters
 
-// ---------------------------------------------------------------- integer form of 32 values
-// Byte orders of the planes, following how a weight word yields its values:
-//   Q8_0: word m = elements 4m .. 4m+3;  nibbles: word 2m = even, 2m+1 = odd elements of 8m..8m+7;
-//   int2: word 4w + k = elements 16w + k + 4b, b = 0..3.
+// ---------------------------------------------------------------- integer form of x and h
+// A row is three planes of bytes (middle, low, high digits) at a pitch of ml_plane(cols).  Byte
+// order within 32 values, following how a weight word yields its values:
+//   nibbles: word 2m = even, 2m+1 = odd elements of 8m..8m+7;  Q8_0: word 2m = elements 4m..4m+3,
+//   2m+1 = 16+4m..;  int2: word 4w + k = elements 16w + k + 4b, b = 0..3.
 enum MlOrder : int { kMlBytes = 0, kMlNibbles = 1, kMlPairs = 2 };
 __host__ __device__ constexpr int ml_order(int fmt) {
   return fmt == BQG_Q8_0 ? kMlBytes : fmt == BQG_I2_ROW ? kMlPairs : kMlNibbles;
 }
+// 48 mod 128: the three planes' 16-byte (and 8-byte) reads of a warp fall into different banks.
+__host__ __device__ constexpr int ml_plane(int cols) { return cols + (48 - cols % 128 + 128) % 128; }
 
-// Four lanes per unit, 8 values each (all lanes of the warp call this; the unit's lanes are
-// consecutive).  rec: the unit's record.
-__device__ __forceinline__ void ml_convert8(const float (&x)[8], int order, uint8_t* rec, bool valid) {
-  const int m = threadIdx.x & 3;
-  float amax = 0.f;
+__device__ __forceinline__ uint32_t ml_pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t sel) {
+  return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
+}
+// 16 consecutive values (segment seg of a row) -> digits in the row's planes.
+__device__ __forceinline__ void ml_digits(const float* src, const uint32_t* most, int order, uint8_t* row, int plane, int seg) {
+  float4 v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  const float inv = amax > 1e-30f ? float(kMlUnitMax) / amax : 0.f;  // below: the unit counts as zeros
-  int q[8];
+  for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(src) + i);
+  const float m = __uint_as_float(*(const volatile uint32_t*)most);
+  const float inv = m > 1e-30f ? float(kMlDigitMax) / m : 0.f;  // below, Inf and NaN: zeros
+  uint32_t t[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = __float2int_rn(x[i] * inv);
-  uint32_t w[3][2];
-  if (order == kMlPairs) {
+  for (int i = 0; i < 4; ++i) {
+    const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      // this lane's two bytes of each word 4 (m / 2) + k; the pair of lanes swaps halves
-      uint32_t half[4];
+    for (int j = 0; j < 4; ++j)  // adding 128 to every digit, with carries, and taking it off without
+      t[4 * i + j] = (uint32_t(__float2int_rn(f[j] * inv)) + 0x808080u) ^ 0x808080u;
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t mine = ((uint32_t(q[k]) >> (16 - 8 * p)) & 0xFFu) |
-                              (((uint32_t(q[4 + k]) >> (16 - 8 * p)) & 0xFFu) << 8);
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-        half[k] = (m & 1) ? (other | (mine << 16)) : (mine | (other << 16));
+  for (int p = 0; p < 3; ++p) {
+    const uint32_t sel = p == 0 ? 0x0051u : p == 1 ? 0x0040u : 0x0062u;
+    uint8_t* at = row + p * plane;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (order == kMlNibbles) {
+        const int o = 8 * (i >> 1) + (i & 1);
+        w[i] = ml_pack(t[o], t[o + 2], t[o + 4], t[o + 6], sel);
+      } else if (order == kMlPairs) {
+        w[i] = ml_pack(t[i], t[i + 4], t[i + 8], t[i + 12], sel);
+      } else {
+        w[i] = ml_pack(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3], sel);
       }
-      w[p][0] = (m & 1) ? half[2] : half[0];  // the even lane stores words k = 0, 1, the odd lane 2, 3
-      w[p][1] = (m & 1) ? half[3] : half[1];
     }
-  } else {
-    const int s = order == kMlNibbles ? 2 : 1;
+    if (order == kMlBytes) {
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      const int sh = 16 - 8 * p;
-      uint32_t b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = (uint32_t(q[i]) >> sh) & 0xFFu;
-      w[p][0] = s == 2 ? (b[0] | b[2] << 8 | b[4] << 16 | b[6] << 24) : (b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24);
-      w[p][1] = s == 2 ? (b[1] | b[3] << 8 | b[5] << 16 | b[7] << 24) : (b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
-    }
-  }
-  if (!valid) return;
-  // words 2m, 2m + 1 of each plane (int2: 4 (m/2) + 2 (m%2) = 2m as well)
-#pragma unroll
-  for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(rec + 32 * p + 8 * m) = make_uint2(w[p][0], w[p][1]);
-  if (m == 0) *reinterpret_cast<float*>(rec + 96) = amax * (1.f / float(kMlUnitMax));
-}
-
-// `units` units of consecutive fp32 values -> consecutive records; lanes i0, i0 + stride, ...
-// (i0 and stride count 8-value segments; a warp's lanes are consecutive).
-__device__ __forceinline__ void ml_convert(const float* src, int units, int order, uint8_t* dst, int i0, int stride) {
-  const int total = 4 * units, padded = (total + 31) / 32 * 32;
-  for (int i = i0; i < padded; i += stride) {
-    float x[8];
-    const bool valid = i < total;
-    if (valid) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(src) + 2 * i);
-      const float4 b = __ldcg(reinterpret_cast<const float4*>(src) + 2 * i + 1);
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(at + 32 * (seg >> 1) + 8 * i + 4 * (seg & 1)) = w[i];
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.f;
+      *reinterpret_cast<uint4*>(at + 16 * seg) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    ml_convert8(x, order, dst + size_t(i >> 2) * kMlRecBytes, valid);
   }
 }
-
-struct MlX {  // one unit in registers
-  uint32_t h[8], m[8], l[8];
-  float s;
-};
-// rec: shared or global memory (generic address).
-__device__ __forceinline__ void ml_load_x(const uint8_t* rec, MlX& X) {
-  const uint4* p = reinterpret_cast<const uint4*>(rec);
-  const uint4 a = p[0], b = p[1], c = p[2], d = p[3], e = p[4], f = p[5];
-  X.h[0] = a.x; X.h[1] = a.y; X.h[2] = a.z; X.h[3] = a.w;
-  X.h[4] = b.x; X.h[5] = b.y; X.h[6] = b.z; X.h[7] = b.w;
-  X.m[0] = c.x; X.m[1] = c.y; X.m[2] = c.z; X.m[3] = c.w;
-  X.m[4] = d.x; X.m[5] = d.y; X.m[6] = d.z; X.m[7] = d.w;
-  X.l[0] = e.x; X.l[1] = e.y; X.l[2] = e.z; X.l[3] = e.w;
-  X.l[4] = f.x; X.l[5] = f.y; X.l[6] = f.z; X.l[7] = f.w;
-  X.s = *reinterpret_cast<const float*>(rec + 96);
+// `rows` rows of `cols` fp32 values, row r's max|v| given by its bits in most[r] (shared or global
+// memory) -> digit rows; segment i of all.  Not inlined: x's call brings the code in for h's.
+__device__ __noinline__ void ml_convert(const float* src, int cols, const uint32_t* most, int order, uint8_t* dst, int i) {
+  const int segs = cols / 16, plane = ml_plane(cols);
+  const int r = i / segs, s = i - r * segs;
+  ml_digits(src + size_t(i) * 16, most + r, order, dst + size_t(r) * 3 * plane, plane, s);
 }
+__device__ __forceinline__ float ml_row_scale(uint32_t most) { return __uint_as_float(most) * (1.f / float(kMlDigitMax)); }
 
-struct MlSum {
-  int h, m, l;
-  __device__ __forceinline__ void word(uint32_t w, const MlX& X, int i) {  // w: four signed bytes
-    h = dp4a_ss(w, X.h[i], h);
-    m = dp4a_su(w, X.m[i], m);
-    l = dp4a_su(w, X.l[i], l);
-  }
-  // |m|, |l| < 2^20 and |h| < 2^19: 256 m + l fits int32
-  __device__ __forceinline__ float value() const { return fmaf(float(h), 65536.f, float(m * 256 + l)); }
+template <int V>
+struct MlInt {
+  static constexpr int value = V;
 };
 
-__host__ __device__ constexpr int ml_unit_bytes(int fmt) {
-  return fmt == BQG_Q8_0 ? 34 : fmt == BQG_Q4_0 ? 18 : fmt == BQG_I4_ROW ? 16 : 8;
+// ---------------------------------------------------------------- products
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
 }
-// The unit at shared-memory byte address u, times X (row scales of int4 / int2 excluded).
-template <int FMT>
-__device__ __forceinline__ float ml_dot(uint32_t u, const MlX& X) {
-  MlSum S{0, 0, 0};
-  if constexpr (FMT == BQG_Q4_0) {
-    const uint32_t a = u & ~3u, sh = (u & 2u) * 8;  // blocks start on even bytes
-    uint32_t v[5];
+// Digits: shared memory (SM) or global memory that this launch wrote before a grid barrier.
+template <bool SM>
+__device__ __forceinline__ uint4 ml_ld128(uint64_t a) {
+  uint4 v;
+  if constexpr (SM) return lds128(uint32_t(a));
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+  return v;
+}
+template <bool SM>
+__device__ __forceinline__ uint2 ml_ld64(uint64_t a) {
+  uint2 v;
+  if constexpr (SM) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(uint32_t(a)));
+  else asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ void ml_mma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__host__ __device__ constexpr bool ml_rowwise(int fmt) { return fmt == BQG_I4_ROW || fmt == BQG_I2_ROW; }
+// Steps of a row: four units of 32 values for the row-scaled formats (a lane reads a whole unit of
+// its rows), else two (the bytes of two blocks are a multiple of 4, so a row's alignment is the same
+// in every step).
+__host__ __device__ constexpr int ml_steps(int fmt, int cols) {
+  return ml_rowwise(fmt) ? (cols / 32 + 3) / 4 : (cols / 32 + 1) / 2;
+}
+
+// Steps [s0, s1) of 16 rows times two tokens.  a0, a1: shared-memory addresses of this lane's two
+// rows (tile rows lane / 4 and + 8); b: its column's digits, at its own part of a step.  out[0..1]:
+// the sums of the lane's rows for token (lane & 2) / 2, in units of the formats' byte forms (row
+// scales excluded); both lanes of a pair get them.  has_b: false in the lanes of a second token that is
+// not there, which load nothing (their columns are never used).
+template <int FMT, bool SM>
+__device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, bool has_b, int units, int s0, int s1,
+                                        float (&out)[2]) {
+  const int q = threadIdx.x & 3;
+  const bool odd = q & 1;
+  if constexpr (ml_rowwise(FMT)) {
+    int c[2][4] = {};  // two chains of MMAs
+    uint4 x0 = {}, x1 = {};
+    constexpr int kLane = FMT == BQG_I4_ROW ? 16 : 8;
+    a0 += kLane * (4 * s0 + q);
+    a1 += kLane * (4 * s0 + q);
+    b += 128 * s0;
+#pragma unroll 2
+    for (int s = s0; s < s1; ++s) {
+      const bool in = 4 * s + q < units;  // past the row's end: zero weights
+      if (has_b) {
+        x0 = ml_ld128<SM>(b);
+        x1 = ml_ld128<SM>(b + 16);
+      }
+      uint32_t w[4][4];                   // the MMAs' A registers
+      if constexpr (FMT == BQG_I4_ROW) {
+        const uint32_t keep = in ? 0xF0F0F0F0u : 0u;
+        const uint4 v0 = lds128(a0), v1 = lds128(a1);
+        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] = lds32(a + 4 * i);
+        for (int j = 0; j < 4; ++j) {
+          w[j][0] = (w0[j] << 4) & keep;
+          w[j][1] = (w1[j] << 4) & keep;
+          w[j][2] = w0[j] & keep;
+          w[j][3] = w1[j] & keep;
+        }
+      } else {
+        const uint32_t keep = in ? 0xC0C0C0C0u : 0u;
+        const uint2 v0 = ml_ld64<true>(a0), v1 = ml_ld64<true>(a1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = __funnelshift_rc(v[i], v[i + 1], 16 + sh);
-      S.word(((w << 4) ^ 0x88888888u) & 0xF0F0F0F0u, X, 2 * i);
-      S.word((w ^ 0x88888888u) & 0xF0F0F0F0u, X, 2 * i + 1);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w0 = j < 2 ? v0.x : v0.y, w1 = j < 2 ? v1.x : v1.y;
+          w[j][0] = (w0 << (j & 1 ? 2 : 6)) & keep;
+          w[j][1] = (w1 << (j & 1 ? 2 : 6)) & keep;
+          w[j][2] = (w0 << (j & 1 ? 0 : 4)) & keep;
+          w[j][3] = (w1 << (j & 1 ? 0 : 4)) & keep;
+        }
+      }
+      ml_mma(c[0], w[0][0], w[0][1], w[0][2], w[0][3], x0.x, x0.y);
+      ml_mma(c[1], w[1][0], w[1][1], w[1][2], w[1][3], x0.z, x0.w);
+      ml_mma(c[0], w[2][0], w[2][1], w[2][2], w[2][3], x1.x, x1.y);
+      ml_mma(c[1], w[3][0], w[3][1], w[3][2], w[3][3], x1.z, x1.w);
+      a0 += 4 * kLane;
+      a1 += 4 * kLane;
+      b += 128;
     }
-    return S.value() * (half_bits_to_float(__funnelshift_r(v[0], v[1], sh)) * X.s);
-  } else if constexpr (FMT == BQG_Q8_0) {
-    const uint32_t a = u & ~3u, sh = (u & 2u) * 8;
-    uint32_t v[9];
-#pragma unroll
-    for (int i = 0; i < 9; ++i) v[i] = lds32(a + 4 * i);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) S.word(__funnelshift_rc(v[i], v[i + 1], 16 + sh), X, i);
-    return S.value() * (half_bits_to_float(__funnelshift_r(v[0], v[1], sh)) * X.s);
-  } else if constexpr (FMT == BQG_I4_ROW) {
-    const uint4 v = lds128(u);
-    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      S.word((q[i] << 4) & 0xF0F0F0F0u, X, 2 * i);
-      S.word(q[i] & 0xF0F0F0F0u, X, 2 * i + 1);
-    }
-    return S.value() * X.s;
+    const float ma = odd ? 65536.f : 256.f, mb = odd ? 0.f : 1.f;
+    out[0] = fmaf(float(c[0][0] + c[1][0]), ma, float(c[0][1] + c[1][1]) * mb);
+    out[1] = fmaf(float(c[0][2] + c[1][2]), ma, float(c[0][3] + c[1][3]) * mb);
   } else {
-    const uint32_t q[2] = {lds32(u), lds32(u + 4)};
+    // 256 m + l of a block in the even lanes.  The odd lanes' second column is the high digit again:
+    // 255 h + h.
+    const int mul = odd ? 255 : 256;
+    float acc[2] = {};
+    constexpr int kUnit = FMT == BQG_Q8_0 ? 34 : 18;
+    a0 += s0 * 2 * kUnit;
+    a1 += s0 * 2 * kUnit;
+    b += 64 * s0;
+    // the lane's word of either block: from two aligned words, since blocks start on even bytes
+    const uint32_t r0 = a0 & 2u, r1 = a1 & 2u;
+    uint32_t e0[2] = {(a0 & ~3u) + 2 * r0 + 4 * q, (a0 & ~3u) + kUnit + 2 + 4 * q};
+    uint32_t e1[2] = {(a1 & ~3u) + 2 * r1 + 4 * q, (a1 & ~3u) + kUnit + 2 + 4 * q};
+    const uint32_t f0[2] = {16 - 8 * r0, 8 * r0}, f1[2] = {16 - 8 * r1, 8 * r1};
+    uint2 xs[2] = {};
+    auto block = [&](int h) {
+      uint2& x = xs[h];
+      if (has_b) x = ml_ld64<SM>(b + 32 * h);
+      const uint32_t h0 = lds16(a0 + kUnit * h), h1 = lds16(a1 + kUnit * h);
+      const uint32_t w0 = __funnelshift_r(lds32(e0[h]), lds32(e0[h] + 4), f0[h]);
+      const uint32_t w1 = __funnelshift_r(lds32(e1[h]), lds32(e1[h] + 4), f1[h]);
+      int c[4] = {0, 0, 0, 0};
+      if constexpr (FMT == BQG_Q8_0) {
+        const uint32_t w2 = __funnelshift_r(lds32(e0[h] + 16), lds32(e0[h] + 20), f0[h]);
+        const uint32_t w3 = __funnelshift_r(lds32(e1[h] + 16), lds32(e1[h] + 20), f1[h]);
+        ml_mma(c, w0, w1, w2, w3, x.x, x.y);
+      } else {
+        ml_mma(c, ((w0 << 4) ^ 0x88888888u) & 0xF0F0F0F0u, ((w1 << 4) ^ 0x88888888u) & 0xF0F0F0F0u,
+               (w0 ^ 0x88888888u) & 0xF0F0F0F0u, (w1 ^ 0x88888888u) & 0xF0F0F0F0u, x.x, x.y);
+      }
+      // |c| <= 32 * 2^14: 256 of them fit int32
+      acc[0] = fmaf(float(c[0] * mul + c[1]), half_bits_to_float(h0), acc[0]);
+      acc[1] = fmaf(float(c[2] * mul + c[3]), half_bits_to_float(h1), acc[1]);
+    };
+#pragma unroll 2
+    for (int s = s0; s < s1; ++s) {
+      block(0);
+      if (2 * s + 1 < units) block(1);
+      a0 += 2 * kUnit;
+      a1 += 2 * kUnit;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) S.word((q[i] << (6 - 2 * k)) & 0xC0C0C0C0u, X, 4 * i + k);
-    return S.value() * X.s;
+      for (int h = 0; h < 2; ++h) {
+        e0[h] += 2 * kUnit;
+        e1[h] += 2 * kUnit;
+      }
+      b += 64;
+    }
+    out[0] = acc[0] * (odd ? 256.f : 1.f);
+    out[1] = acc[1] * (odd ? 256.f : 1.f);
   }
-}
-
-// What a row's plane sums are multiplied by: the byte form's factor and the row scale, if any.
-__device__ __forceinline__ float ml_scale(int fmt, const uint8_t* scales, int row) {
-  if (fmt == BQG_Q8_0) return 1.f;
-  if (fmt == BQG_Q4_0) return 1.f / 16.f;
-  return __ldg(reinterpret_cast<const float*>(scales) + row) * (fmt == BQG_I2_ROW ? 1.f / 64.f : 1.f / 16.f);
-}
-
-// Sums of four values over the warp: every lane gets the total of v[lane & 3].
-__device__ __forceinline__ float ml_reduce4(const float (&v)[4]) {
-  const int lane = threadIdx.x & 31;
-  const bool odd = lane & 1, high = lane & 2;
-  const float a = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-  const float b = (odd ? v[3] : v[2]) + __shfl_xor_sync(0xffffffffu, odd ? v[2] : v[3], 1);
-  float s = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
-  s += __shfl_xor_sync(0xffffffffu, s, 4);
-  s += __shfl_xor_sync(0xffffffffu, s, 8);
-  s += __shfl_xor_sync(0xffffffffu, s, 16);
-  return s;
+  out[0] += __shfl_xor_sync(0xffffffffu, out[0], 1);
+  out[1] += __shfl_xor_sync(0xffffffffu, out[1], 1);
 }
 
 // ---------------------------------------------------------------- parameters
@@ -233,11 +284,13 @@ struct MlFam {           // matrices of the routed experts (0) or of the shared 
   int fmt, inter;
   int rb1, rb2;          // row bytes of gate / up and of down
   int off1, off2;        // byte offset of the fp32 row scales (int4, int2) of gate / up, down
+  int second1, second2;  // place of an item's second block of rows
   int nf, nr;            // features per item of phase 1 (a gate and an up row each), rows per item of phase 2
-  int second;            // phase 1: slot offset of the up rows
-  int share;             // most features of an expert that one CTA has
-  int slices;            // of a row of down
-  int x_order;           // which of the two x record sets it reads
+  int tiles;             // of an item of phase 2
+  int items;             // of an expert in phase 1
+  int parts1, parts2;    // of an item's k range
+  int y_first, y_step;   // place of the down sums: [pair][part][rows_cta]
+  int x_set;             // which of the digit forms of x it reads
 };
 
 struct MlParams {
@@ -248,43 +301,41 @@ struct MlParams {
   int32_t* idx;          // or null
   float* w;
   int tokens, n_experts, top_k, hidden, act, has_shared;
-  int slices;            // of a row of gate / up
   // workspace
-  uint32_t* bar;         // barrier counters, one per 128 bytes, zero between calls
+  uint32_t* bar;         // barrier counters, one per 128 bytes, and the rows' max|h|: zero between calls
   float* logits;         // [tokens][n_experts]
   float* h[2];           // [pairs][inter], [tokens][shared inter]
-  uint8_t* xrec[2];      // global x records (when they do not fit shared memory)
+  uint8_t* xrec[2];      // digit rows in global memory (when they do not fit shared memory)
   uint8_t* hrec[2];
-  float* sums;           // global partial sums of every CTA (when they do not fit shared memory)
   int x_sets;            // 1 or 2 byte orders of x
   int set_order[2];
-  int x_smem, h_smem;    // the records are in shared memory
+  int x_smem, h_smem;    // the digit rows are in shared memory
   // shared memory layout
-  int slots, slot_bytes, rec_off, sum_off, rows_cta;
-  int sums_smem;
-  int sums_cta;          // partial sums of a CTA (floats)
+  int ring_bytes, rec_off, sum_off, y_off, rows_cta;
+  int parts_max;         // most parts of an item of phase 1
 };
 
 struct MlShared {
-  uint64_t full[kMlMaxSlots], empty[kMlMaxSlots];
-  uint64_t topk_ready, list_ready;
-  int4 desc[kMlMaxSlots][2];
-  int seq[kMlMaxSlots];  // the item in the slot
-  int next;
+  uint64_t full[kMlSlots], done[kMlSlots], empty[kMlSlots];
+  uint64_t topk_ready, h_ready;
+  int4 desc[kMlSlots][3];
+  int seq[kMlSlots];     // the item in the slot
+  int start[kMlSlots];   // its place in the ring
   int abort;
-  int n_active, n_shared1, n1, tasks2;
+  int n_active, n1;      // touched experts, the CTA's items of phase 1
   float red[kMlWarps][kMlMaxTokens];
+  uint32_t xmax[kMlMaxTokens];
+  uint32_t hmax[kMlMaxPairs + kMlMaxTokens];
+  uint2 mark[BQG_MAX_EXPERTS];         // an expert's pairs, as bits
   int sel_e[kMlMaxPairs];
   float sel_w[kMlMaxPairs];
-  int act_e[kMlMaxPairs];
-  uint32_t act_mask[kMlMaxPairs][2];  // the pairs of a touched expert
-  int first[kMlMaxPairs];
-  int pair_a[kMlMaxPairs];            // a pair's expert in act_e
+  int act_e[kMlMaxPairs];              // the touched experts in increasing order (one token: in slot order)
+  int act_first[kMlMaxPairs + 1];      // their pairs: order[first .. first of the next)
+  int order[kMlMaxPairs + kMlMaxTokens];  // pair | token << 8; behind kMlMaxPairs the shared expert's, tokens in turn
 };
 
 // ---------------------------------------------------------------- grid barriers
 __device__ __forceinline__ void ml_arrive(uint32_t* c) {
-  __threadfence();
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(c) : "memory");
 }
 __device__ __forceinline__ bool ml_wait(uint32_t* c, uint32_t n) {
@@ -299,17 +350,33 @@ __device__ __forceinline__ bool ml_wait(uint32_t* c, uint32_t n) {
     }
   }
 }
+// Until item i is in its slot; only then does the parity of the slot's barriers tell the item's own phase.
+__device__ __forceinline__ bool ml_wait_seq(int* seq, int i) {
+  unsigned long long since = 0;
+  for (;;) {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(seq)) : "memory");
+    if (v == i) return true;
+    const unsigned long long now = globaltimer_ns();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitNs) {
+      flag_error(BQG_DEVERR_TIMEOUT);
+      return false;
+    }
+    __nanosleep(40);
+  }
+}
+// All warps: the lists are made.  A hardware barrier, since warps that poll slow down the one that selects.
+// The warp that made them only arrives: it has items of the shared expert to finish before the others come.
+__device__ __forceinline__ void ml_list_arrive() { asm volatile("bar.arrive 3, %0;" ::"n"(kMlThreads) : "memory"); }
+__device__ __forceinline__ void ml_list_sync() { asm volatile("bar.sync 3, %0;" ::"n"(kMlThreads) : "memory"); }
 __device__ __forceinline__ void ml_consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kMlConsumers) : "memory"); }
 
-// ---------------------------------------------------------------- work split
 __device__ __forceinline__ int ml_share(int n, int b) { return int((long long)n * b / gridDim.x); }
 __device__ __forceinline__ int ml_div_up(int a, int b) { return (a + b - 1) / b; }
-// Features [f0, f1) of the a-th touched expert that this CTA has.  The experts' shares are turned
-// against one another, so that the CTAs with the larger ones differ.
-__device__ __forceinline__ void ml_features(int inter, int a, int& f0, int& f1) {
-  const int b = int((blockIdx.x + 61u * unsigned(a)) % gridDim.x);
-  f0 = ml_share(inter, b);
-  f1 = ml_share(inter, b + 1);
+// How many of the items [0, n), dealt out in turn, the CTA has.
+__device__ __forceinline__ int ml_dealt(int n) {
+  return int(blockIdx.x) < n ? (n - 1 - int(blockIdx.x)) / int(gridDim.x) + 1 : 0;
 }
 
 // ---------------------------------------------------------------- selection of the experts
@@ -317,304 +384,423 @@ __device__ __forceinline__ void ml_features(int inter, int a, int& f0, int& f1) 
 // weights e^(l - max) over the selected ones' sum, which is the renormalised softmax.
 __device__ __forceinline__ void ml_topk(const float* logits, int E, int k, int* sel_e, float* sel_w) {
   const int lane = threadIdx.x & 31;
-  float v[8];
-  uint32_t key[8];
-  uint32_t taken = 0;
+  uint32_t key[8];  // increasing with the logit; 0: none or taken, 1: NaN
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int e = lane + 32 * i;
-    v[i] = e < E ? __ldcg(logits + e) : 0.f;
-    const uint32_t u = __float_as_uint(v[i] == 0.f ? 0.f : v[i]);
-    key[i] = v[i] != v[i] ? 0u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    if (e >= E) taken |= 1u << i;
+    const float v = e < E ? __ldcg(logits + e) : 0.f;
+    const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
+    key[i] = e >= E ? 0u : v != v ? 1u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
   }
-  float mine = 0.f, top = 0.f, sum = 0.f;  // lane j keeps slot j
+  uint32_t mine = 1u;  // lane j keeps slot j
   int mine_e = 0;
-  for (int j = 0; j < k; ++j) {
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {  // code that runs once comes from L2: short loops, here and below
     uint32_t bk = 0;
-    int be = 0x7fffffff;
-    float bv = 0.f;
+    int bi = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (!(taken >> i & 1u) && (be == 0x7fffffff || key[i] > bk)) {
+      if (key[i] > bk) {
         bk = key[i];
-        be = lane + 32 * i;
-        bv = v[i];
+        bi = i;
       }
     const uint32_t most = __reduce_max_sync(0xffffffffu, bk);
-    const unsigned e = __reduce_min_sync(0xffffffffu, bk == most ? unsigned(be) : 0x7fffffffu);
-    const float val = __shfl_sync(0xffffffffu, bv, int(e & 31));
-    if ((e & 31u) == unsigned(lane)) taken |= 1u << (e >> 5);
-    if (j == 0) top = val;
-    const float p = expf(val - top);
-    sum += p;
+    const unsigned e = __reduce_min_sync(0xffffffffu, bk == most ? unsigned(lane + 32 * bi) : 0x7fffffffu);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e == unsigned(lane + 32 * i)) key[i] = 0u;
     if (lane == j) {
-      mine = p;
+      mine = most;
       mine_e = int(e);
     }
   }
+  const float v = mine == 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float((mine & 0x80000000u) ? mine ^ 0x80000000u : ~mine);
+  const float p = expf(v - __shfl_sync(0xffffffffu, v, 0));
+  float sum = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) sum += __shfl_sync(0xffffffffu, p, j);
   if (lane < k) {
     sel_e[lane] = mine_e;
-    sel_w[lane] = mine / sum;
+    sel_w[lane] = p / sum;
   }
 }
 
-// The touched experts in increasing order with their pairs (one warp).
-__device__ __forceinline__ void ml_list(MlShared& S, int pairs) {
+// The touched experts with their pairs (one warp).
+__device__ __forceinline__ void ml_list(MlShared& S, int tokens, int top_k) {
+  const int pairs = tokens * top_k;
   const int lane = threadIdx.x & 31;
-  for (int a = lane; a < kMlMaxPairs; a += 32) S.act_mask[a][0] = S.act_mask[a][1] = 0u;
-  __syncwarp();
-  int distinct = 0;
-  for (int p = lane; p < (pairs + 31) / 32 * 32; p += 32) {
-    const int e = p < pairs ? S.sel_e[p] : -1;
-    bool first = p < pairs;  // the expert's first pair
-    for (int q = 0; q < pairs; ++q) first = first && !(q < p && S.sel_e[q] == e);
-    if (p < pairs) S.first[p] = first;
-    distinct += __popc(__ballot_sync(0xffffffffu, first));
-  }
-  __syncwarp();
-  for (int p = lane; p < pairs; p += 32) {
-    const int e = S.sel_e[p];
-    int rank = 0;
-    for (int q = 0; q < pairs; ++q) rank += S.first[q] && S.sel_e[q] < e;
-    S.act_e[rank] = e;
-    S.pair_a[p] = rank;
-    atomicOr(&S.act_mask[rank][p >> 5], 1u << (p & 31));
-  }
-  if (lane == 0) S.n_active = distinct;
-  __syncwarp();
-}
-
-// ---------------------------------------------------------------- items
-// Slice j of an item for every token of its expert.  Phase 1: n gate rows at shared-memory address
-// `at` and n up rows at `at + up` (row pitch rb), sums [pair][feature][gate, up][slice]; phase 2
-// (up = 0): n rows, sums [pair][row][slice].  X: the slice's x, and `held` the record that it was
-// loaded from (a warp's next item often takes the same one).  Rows are taken four at a time, the
-// last again where there are fewer: one copy of the loop body per format, since the warps of an SM
-// run it out of step and share its instruction cache.
-template <int FMT>
-__device__ __forceinline__ void ml_item(uint32_t at, uint32_t up, int rb, int n, int units, int slices, int j,
-                                        uint32_t m0, uint32_t m1, int per_token, const uint8_t* recs, float* sums,
-                                        int pair_step, MlX& X, const uint8_t*& held) {
-  const int lane = threadIdx.x & 31;
-  const int c = min(j * 32 + lane, units - 1);
-  const int rows = up ? 2 * n : n, step = up ? 2 * slices : slices;
-  at += uint32_t(c) * ml_unit_bytes(FMT);
-  while (m0 | m1) {
-    int p;
-    if (m0) {
-      p = __ffs(m0) - 1;
-      m0 &= m0 - 1;
-    } else {
-      p = 31 + __ffs(m1);
-      m1 &= m1 - 1;
+  if (tokens == 1) {  // all different
+    if (lane < pairs) {
+      S.act_e[lane] = S.sel_e[lane];
+      S.order[lane] = lane;
     }
-    const uint8_t* rec = recs + (size_t(p / per_token) * units + c) * kMlRecBytes;
-    if (rec != held) {
-      ml_load_x(rec, X);
-      if (j * 32 + lane >= units) X.s = 0.f;  // a lane past the row's end: the last unit, times zero
-      held = rec;
-    }
+    if (lane <= pairs) S.act_first[lane] = lane;
+    if (lane == 0) S.n_active = pairs;
     __syncwarp();
-    float* sum = sums + size_t(p) * pair_step + j;
-#pragma unroll 1
-    for (int r = 0; r < rows; r += 4) {
-      float v[4];
+    return;
+  }
+  for (int p = lane; p < pairs; p += 32) atomicOr(p < 32 ? &S.mark[S.sel_e[p]].x : &S.mark[S.sel_e[p]].y, 1u << (p & 31));
+  __syncwarp();
+  int mine = 0;  // of experts 8 lane ..: touched experts << 16 | pairs
+  for (int i = 0; i < 8; ++i) {
+    const uint2 m = S.mark[8 * lane + i];
+    const int n = __popc(m.x) + __popc(m.y);
+    mine += n > 0 ? (1 << 16) + n : 0;
+  }
+  int upto = mine;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int q = min(r + i, rows - 1);
-        v[i] = ml_dot<FMT>(at + (q < n ? uint32_t(q * rb) : up + uint32_t((q - n) * rb)), X);
-      }
-      const float s = ml_reduce4(v);
-      const int q = r + lane;
-      if (lane < 4 && q < rows) sum[q < n ? q * step : (q - n) * step + slices] = s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  int a = (upto - mine) >> 16, at = (upto - mine) & 0xffff;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    uint32_t lo = S.mark[8 * lane + i].x, hi = S.mark[8 * lane + i].y;
+    if (!(lo | hi)) continue;
+    S.act_e[a] = 8 * lane + i;
+    S.act_first[a++] = at;
+    while (lo | hi) {
+      const int p = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+      if (lo) lo &= lo - 1;
+      else hi &= hi - 1;
+      S.order[at++] = p | (p / top_k) << 8;
     }
   }
+  if (lane == 31) {
+    S.n_active = a;
+    S.act_first[a] = at;
+  }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- the kernel
 __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_constant__ MlParams P) {
-  extern __shared__ __align__(128) uint8_t smem[];  // ring, records, partial sums
+  extern __shared__ __align__(128) uint8_t smem[];  // ring, digit rows, partial sums
   __shared__ MlShared S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = int(blockIdx.x), G = int(gridDim.x);
   const int pairs = P.tokens * P.top_k;
   uint8_t* rec_s = smem + P.rec_off;
-  float* sums = P.sums_smem ? reinterpret_cast<float*>(smem + P.sum_off) : P.sums + size_t(b) * P.sums_cta;
-
-  // the CTA's shares
-  const int sf0 = P.has_shared ? ml_share(P.fam[1].inter, b) : 0, sf1 = P.has_shared ? ml_share(P.fam[1].inter, b + 1) : 0;
-  const int hr0 = ml_share(P.hidden, b), hr1 = ml_share(P.hidden, b + 1);
+  float* sums = reinterpret_cast<float*>(smem + P.sum_off);    // phase 1: [slot][part][pair of the item][16]
+  float* y_sums = reinterpret_cast<float*>(smem + P.y_off);    // phase 2: [pairs, then tokens][part][rows_cta]
+  const int hr0 = ml_share(P.hidden, b), rows = ml_share(P.hidden, b + 1) - hr0;
+  const int n_shared = P.has_shared ? P.fam[1].items : 0;      // phase 1: the shared expert's items come first
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < P.slots; ++i) {
+    for (int i = 0; i < kMlSlots; ++i) {
       mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], kMlArrivals);
+      mbar_init(&S.empty[i], 1);
+      mbar_init(&S.done[i], kMlWarps);
       S.seq[i] = -1;
     }
     mbar_init(&S.topk_ready, uint32_t(P.tokens));
-    mbar_init(&S.list_ready, 1);
-    S.next = 0;
+    mbar_init(&S.h_ready, kMlHelpers);
     S.abort = 0;
-    S.n_shared1 = P.has_shared ? ml_div_up(sf1 - sf0, P.fam[1].nf) : 0;
     fence_barrier_init();
+  }
+  for (int i = threadIdx.x; i < BQG_MAX_EXPERTS; i += kMlThreads) S.mark[i] = make_uint2(0u, 0u);
+  if (threadIdx.x < kMlMaxTokens) {
+    S.xmax[threadIdx.x] = 0u;
+    S.order[kMlMaxPairs + threadIdx.x] = (pairs + threadIdx.x) | threadIdx.x << 8;
   }
   __syncthreads();
 
   if (warp == kMlWarps) {
-    // ------------------------------------------------ producer (one lane)
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_first();
-      int i = 0;
-      bool ok = true;
-      // rows [r0, r0 + n) of a matrix to slot offset `at`; returns the data's offset in the slot
-      auto rows_in = [&](uint8_t* slot, int at, const uint8_t* base, int rb, int rows, int r0, int n, uint32_t& bytes,
-                         uint64_t* bar, bool issue) -> int {
-        const uintptr_t wbeg = reinterpret_cast<uintptr_t>(base);
-        const uintptr_t src = wbeg + size_t(r0) * rb, end = src + size_t(n) * rb;
-        const uintptr_t a0 = src & ~uintptr_t(15), lim = (wbeg + size_t(rows) * rb) & ~uintptr_t(15);
-        uintptr_t a1 = (end + 15) & ~uintptr_t(15);
-        if (a1 > lim) a1 = lim;
-        if (a1 < a0) a1 = a0;
-        uint8_t* dst = slot + at;
-        if (!issue) {  // bytes past the matrix's last whole 16: plain loads
-          for (uintptr_t c = (a1 > src ? a1 : src); c < end; ++c) dst[c - a0] = *reinterpret_cast<const uint8_t*>(c);
-          bytes += uint32_t(a1 - a0);
-        } else if (a1 > a0) {
-          bulk_g2s(dst, reinterpret_cast<const void*>(a0), uint32_t(a1 - a0), bar, pol);
-        }
-        return at + int(src - a0);
-      };
-      auto put = [&](int type, int a, const MlFam& F, int e, int r0, int n) -> bool {
-        const int slot = i % P.slots;
-        if (i >= P.slots && !mbar_wait(&S.empty[slot], uint32_t(i / P.slots - 1) & 1u)) return false;
-        fence_proxy_async_smem();
-        uint8_t* at = smem + size_t(slot) * P.slot_bytes;
-        uint64_t* bar = &S.full[slot];
-        uint32_t bytes = 0;
-        int o0, o1 = 0;
-        const bool first = type < 2;
-        const uint8_t* m0 = first ? F.gate + (long long)e * F.gate_stride : F.down + (long long)e * F.down_stride;
-        const uint8_t* m1 = F.up + (long long)e * F.up_stride;
-        const int rb = first ? F.rb1 : F.rb2, rows = first ? F.inter : P.hidden;
-        o0 = rows_in(at, 0, m0, rb, rows, r0, n, bytes, bar, false);
-        if (first) o1 = rows_in(at, F.second, m1, rb, rows, r0, n, bytes, bar, false);
-        S.desc[slot][0] = make_int4(type, a, r0, n);
-        S.desc[slot][1] = make_int4(o0, o1, e, 0);
-        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&S.seq[slot])), "r"(i) : "memory");
-        if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
-        else mbar_arrive(bar);
-        rows_in(at, 0, m0, rb, rows, r0, n, bytes, bar, true);
-        if (first) rows_in(at, F.second, m1, rb, rows, r0, n, bytes, bar, true);
-        ++i;
-        return true;
-      };
-      // phase 1: the shared expert's features, then the routed ones (types 0 / 1: routed / shared)
-      for (int f = sf0; f < sf1 && ok; f += P.fam[1].nf) ok = put(1, 0, P.fam[1], 0, f, min(P.fam[1].nf, sf1 - f));
-      ok = ok && mbar_wait(&S.list_ready, 0) && !*(volatile int*)&S.abort;
-      if (ok) {
-        const int na = S.n_active;
-        for (int a = 0; a < na && ok; ++a) {
-          int f0, f1;
-          ml_features(P.fam[0].inter, a, f0, f1);
-          for (int f = f0; f < f1 && ok; f += P.fam[0].nf) ok = put(0, a, P.fam[0], S.act_e[a], f, min(P.fam[0].nf, f1 - f));
-        }
-        // phase 2 (types 2 / 3: routed / shared)
-        if (P.has_shared)
-          for (int r = hr0; r < hr1 && ok; r += P.fam[1].nr) ok = put(3, 0, P.fam[1], 0, r, min(P.fam[1].nr, hr1 - r));
-        for (int a = 0; a < na && ok; ++a)
-          for (int r = hr0; r < hr1 && ok; r += P.fam[0].nr)
-            ok = put(2, a, P.fam[0], S.act_e[a], r, min(P.fam[0].nr, hr1 - r));
-      }
-      if (!ok) {  // a bounded wait gave up: wait (bounded) for the copies in flight
-        *(volatile int*)&S.abort = 1;
-        for (int q = (i > P.slots ? i - P.slots : 0); q < i; ++q)
-          mbar_wait(&S.full[q % P.slots], uint32_t(q / P.slots) & 1u);
-      }
-    }
-  } else if (warp == kMlWarps + 1) {
-    // ------------------------------------------------ router warp: selection of token 0 .. and the lists
+    // ------------------------------------------------ producer
+    const uint64_t pol = policy_evict_first();
+    int i = 0, tail = 0, head = 0, oldest = 0;  // items [tail, i) hold the ring from `oldest` to `head`
     bool ok = true;
-    if (P.tokens == 1) {
-      if (lane == 0) ok = ml_wait(P.bar, uint32_t(G));
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (ok) ml_topk(P.logits, P.n_experts, P.top_k, S.sel_e, S.sel_w);
-    } else {
-      ok = mbar_wait(&S.topk_ready, 0) && !*(volatile int*)&S.abort;
-    }
-    __syncwarp();
-    if (ok) {
-      ml_list(S, pairs);
-      const int na = S.n_active;
-      int n1 = 0;
-      for (int a = lane; a < na; a += 32) {
-        int f0, f1;
-        ml_features(P.fam[0].inter, a, f0, f1);
-        n1 += ml_div_up(f1 - f0, P.fam[0].nf);
+    int n1 = 1 << 30;  // items of phase 1, once known
+    // One copy of rows [r0, r0 + n) of a matrix to ring offset `at`: its 16-byte whole; the bytes past
+    // the matrix's last whole 16 by plain loads.
+    struct Copy {
+      uintptr_t from;
+      uint32_t bytes;
+      int off;
+    };
+    auto plan = [&](const uint8_t* base, int rb, int all, int r0, int n, int at) -> Copy {
+      const uintptr_t src = reinterpret_cast<uintptr_t>(base) + uint32_t(r0 * rb);
+      Copy c;
+      c.off = int(src & 15);
+      c.from = src - c.off;
+      c.bytes = uint32_t(c.off + n * rb + 15) & ~15u;
+      if (n == 0) {
+        c.bytes = 0;
+      } else if (r0 + n == all) {
+        const uint32_t whole = uint32_t(c.off + n * rb) & ~15u;
+#pragma unroll 1
+        for (uint32_t k = whole + lane; k < uint32_t(c.off + n * rb); k += 32) smem[at + k] = reinterpret_cast<const uint8_t*>(c.from)[k];
+        c.bytes = whole;
       }
-      n1 = __reduce_add_sync(0xffffffffu, n1);
+      return c;
+    };
+    // An item is two blocks of rows: n of gate and of up, or the two halves of n rows of down.
+    auto put = [&](bool first, const MlFam& F, int e, int r0, int n, int p0, int np) -> bool {
+      const int rb = first ? F.rb1 : F.rb2, second = first ? F.second1 : F.second2;
+      const int na = first ? n : (n + 1) / 2, nb = n - (first ? 0 : na);
+      const int need = (second + nb * rb + 30 + 127) & ~127;
+      // a place; a full and a wrapped ring look alike: head <= oldest with items in it
+      for (;;) {
+        if (i == tail) head = oldest = 0;
+        if (i - tail < kMlSlots) {
+          const bool wrapped = i > tail && head <= oldest;
+          if (!wrapped && head + need > P.ring_bytes && need <= oldest) head = 0;
+          if (head + need <= (i > tail && head <= oldest ? oldest : P.ring_bytes)) break;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&S.done[tail % kMlSlots], uint32_t(tail / kMlSlots) & 1u))) return false;
+        ++tail;
+        if (tail < i) oldest = S.start[tail % kMlSlots];
+      }
+      // the slot's sums, where the helpers read them
+      const int last = i - kMlSlots;
+      if (last >= 0 && last < n1 &&
+          !__all_sync(0xffffffffu, mbar_wait(&S.empty[i % kMlSlots], uint32_t(last / kMlSlots) & 1u)))
+        return false;
+      fence_proxy_async_smem();
+      const int slot = i % kMlSlots;
+      uint64_t* bar = &S.full[slot];
+      const uint8_t* m0 = first ? F.gate + e * F.gate_stride : F.down + e * F.down_stride;
+      const uint8_t* m1 = first ? F.up + e * F.up_stride : m0;
+      const int all = first ? F.inter : P.hidden, r1 = first ? r0 : r0 + na;
+      const Copy c0 = plan(m0, rb, all, r0, na, head);
+      const Copy c1 = plan(m1, rb, all, r1, nb, head + second);
       if (lane == 0) {
-        const int rows = hr1 - hr0;
-        S.n1 = S.n_shared1 + n1;
-        S.tasks2 = (P.has_shared ? ml_div_up(rows, P.fam[1].nr) * P.fam[1].slices : 0) +
-                   na * ml_div_up(rows, P.fam[0].nr) * P.fam[0].slices;
+        S.start[slot] = head;
+        S.desc[slot][0] = make_int4(r0, n, p0, np);
+        S.desc[slot][1] = make_int4(head + c0.off, nb > 0 ? head + second + c1.off : head + c0.off, na, nb);
+        if (ml_rowwise(F.fmt)) {  // where the rows' scales are
+          const int off = first ? F.off1 : F.off2;
+          const unsigned long long q0 = reinterpret_cast<unsigned long long>(m0) + uint32_t(off + 4 * r0);
+          const unsigned long long q1 = reinterpret_cast<unsigned long long>(m1) + uint32_t(off + 4 * r1);
+          S.desc[slot][2] = make_int4(int(q0), int(q0 >> 32), int(q1), int(q1 >> 32));
+        }
       }
-      if (b == 0 && P.idx != nullptr)
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&S.seq[slot])), "r"(i) : "memory");
+        if (c0.bytes + c1.bytes > 0) mbar_arrive_expect_tx(bar, c0.bytes + c1.bytes);
+        else mbar_arrive(bar);
+        if (c0.bytes) bulk_g2s(smem + head, reinterpret_cast<const void*>(c0.from), c0.bytes, bar, pol);
+        if (c1.bytes) bulk_g2s(smem + head + second, reinterpret_cast<const void*>(c1.from), c1.bytes, bar, pol);
+      }
+      head += need;
+      ++i;
+      return true;
+    };
+    // One call in a loop for all four kinds of items: phase 1 shared, routed, phase 2 shared, routed.
+    int id = b, active = 0;
+    bool listed = false;
+    for (int pass = P.has_shared ? 0 : 1; pass < 4 && ok; ++pass) {
+      if (pass == 1) {
+        ml_list_sync();
+        listed = true;
+        ok = !*(volatile int*)&S.abort;
+        if (!ok) break;
+        active = S.n_active;
+        n1 = S.n1;
+      }
+      if (pass == 2 && !P.has_shared) continue;
+      const bool first = pass < 2;
+      const MlFam& F = P.fam[pass & 1 ? 0 : 1];
+      int a = 0, r = 0;
+      for (;;) {
+        int n = F.nf;
+        if (first) {
+          if (id >= n_shared + (pass == 1 ? active * F.items : 0)) break;
+          const int k = pass == 1 ? id - n_shared : id;
+          a = k / F.items;
+          r = (k - a * F.items) * F.nf;
+          id += G;
+        } else {
+          if (a >= (pass == 3 ? active : 1) || rows == 0) break;
+          n = min(F.nr, rows - r);
+        }
+        const bool routed = pass & 1;
+        const int p0 = routed ? S.act_first[a] : kMlMaxPairs;
+        ok = put(first, F, routed ? S.act_e[a] : 0, first ? r : hr0 + r, n, p0,
+                 routed ? S.act_first[a + 1] - p0 : P.tokens);
+        if (!ok) break;
+        if (!first) {
+          r += n;
+          if (r >= rows) {
+            r = 0;
+            ++a;
+          }
+        }
+      }
+    }
+    if (!listed) ml_list_sync();
+    if (!ok) {  // a bounded wait gave up: wait (bounded) for the copies in flight
+      if (lane == 0) *(volatile int*)&S.abort = 1;
+      for (int k = tail; k < i; ++k) mbar_wait(&S.full[k % kMlSlots], uint32_t(k / kMlSlots) & 1u);
+    }
+  } else if (warp > kMlWarps) {
+    // ------------------------------------------------ helpers
+    // The first one: selection of one token, and the lists.
+    bool ok = true;
+    if (warp == kMlWarps + 1) {
+      if (P.tokens == 1) {
+        // twice: before the barrier on any numbers, which brings the code in from L2
+        for (int go = 0; go < 2; ++go) {
+          if (go) {
+            if (lane == 0) ok = ml_wait(P.bar, uint32_t(G));
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+          }
+          if (ok) {
+            ml_topk(go ? P.logits : P.R, P.n_experts, P.top_k, S.sel_e, S.sel_w);
+            __syncwarp();
+            ml_list(S, 1, P.top_k);
+          }
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.topk_ready, 0)) && !*(volatile int*)&S.abort;
+        __syncwarp();
+        if (ok) ml_list(S, P.tokens, P.top_k);
+      }
+      if (lane == 0) {
+        if (ok) S.n1 = ml_dealt(n_shared + S.n_active * P.fam[0].items);
+        else *(volatile int*)&S.abort = 1;
+      }
+      __syncwarp();
+      if (ok && b == 0 && P.idx != nullptr)
         for (int p = lane; p < pairs; p += 32) {
           P.idx[p] = S.sel_e[p];
           P.w[p] = S.sel_w[p];
         }
-    } else if (lane == 0) {
-      *(volatile int*)&S.abort = 1;
     }
+    // All of them, the items of phase 1 in turn: the parts added in order, h, the slot freed.
+    const int ns = ml_dealt(n_shared), step = P.tokens * 16;
+    int end = ns;
+    bool listed = false;
+    ok = true;
+    auto need_list = [&]() {
+      if (!listed) ml_list_sync();
+      listed = true;
+      end = S.n1;
+      ok = ok && !*(volatile int*)&S.abort;
+    };
+    if (warp == kMlWarps + 1) {
+      ml_list_arrive();
+      listed = true;
+      need_list();
+    }
+    for (int i = warp - kMlWarps - 1;; i += kMlHelpers) {
+      if (i >= ns && !listed) need_list();
+      if (!ok || i >= end) break;
+      const int slot = i % kMlSlots;
+      ok = __all_sync(0xffffffffu, ml_wait_seq(&S.seq[slot], i)) &&
+           __all_sync(0xffffffffu, mbar_wait(&S.done[slot], uint32_t(i / kMlSlots) & 1u));
+      if (!ok) break;
+      const int fam = i < ns ? 1 : 0;
+      const MlFam& F = P.fam[fam];
+      const int4 d = ld_desc(&S.desc[slot][0]);
+      const int r0 = d.x, n = d.y, np = d.w, parts = F.parts1, fam_pairs = fam ? pairs : 0;
+      const float* in = sums + slot * P.parts_max * step;
+#pragma unroll 1
+      for (int l = lane; l < (np * 8 + 31) / 32 * 32; l += 32) {
+        const int k = l >> 3, f = l & 7;
+        const int p = S.order[d.z + min(k, np - 1)];
+        uint32_t most = 0u;
+        if (k < np && f < n) {
+          float gs = 0.f, us = 0.f;
+#pragma unroll 4
+          for (int c = 0; c < parts; ++c) {
+            gs += in[c * step + k * 16 + f];
+            us += in[c * step + k * 16 + 8 + f];
+          }
+          const float sx = ml_row_scale(S.xmax[p >> 8]);
+          const float h = act_fn(P.act, gs * sx) * (us * sx);
+          P.h[fam][size_t((p & 255) - fam_pairs) * F.inter + r0 + f] = h;
+          most = __float_as_uint(h) & 0x7fffffffu;
+        }
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 4));
+        if (f == 0 && k < np) atomicMax(P.bar + kMlHmax + (p & 255), most);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.empty[slot]);
+    }
+    if (!listed) need_list();
+    if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.list_ready);
+    if (lane == 0) mbar_arrive(&S.h_ready);
   } else {
     // ------------------------------------------------ consumers
     const int tid = threadIdx.x;
-    const int units = P.hidden / 32;
-    // x in integer form: the CTA's own copy, or its share of the copy in global memory
-    for (int s = 0; s < P.x_sets; ++s) {
-      uint8_t* dst = P.x_smem ? rec_s + size_t(s) * P.tokens * units * kMlRecBytes : P.xrec[s];
-      ml_convert(P.x, P.tokens * units, P.set_order[s], dst, P.x_smem ? tid : b * kMlConsumers + tid,
-                 P.x_smem ? kMlConsumers : G * kMlConsumers);
-    }
-    // logits of experts b, b + G, ...: the warps split the row
-    const int h4 = P.hidden / 4;
-    for (int e = b; e < P.n_experts; e += G) {
+    // logits of experts b and b + G (half of the warps each when there are two), and max|x| of all tokens
+    {
+      const int two = b + G < P.n_experts ? 1 : 0;
+      const int n = kMlConsumers >> two, grp = tid >= n ? 1 : 0, e = b + grp * G;
+      const bool has = e < P.n_experts;
+      const int h4 = P.hidden / 4;
+      const float4* r4 = reinterpret_cast<const float4*>(P.R + size_t(has ? e : 0) * P.hidden);
       float acc[kMlMaxTokens];
+      uint32_t most[kMlMaxTokens];
 #pragma unroll
-      for (int t = 0; t < kMlMaxTokens; ++t) acc[t] = 0.f;
-      const float4* r4 = reinterpret_cast<const float4*>(P.R + size_t(e) * P.hidden);
-#pragma unroll 2
-      for (int k = tid; k < h4; k += kMlConsumers) {
-        const float4 r = __ldg(r4 + k);
+      for (int t = 0; t < kMlMaxTokens; ++t) {
+        acc[t] = 0.f;
+        most[t] = 0u;
+      }
+      for (int k0 = tid - grp * n; k0 < h4; k0 += 4 * n) {
+        float4 r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = has && k0 + j * n < h4 ? __ldg(r4 + k0 + j * n) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int t = 0; t < kMlMaxTokens; ++t)
           if (t < P.tokens) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(P.x + size_t(t) * P.hidden) + k);
-            acc[t] = fmaf(r.x, v.x, acc[t]);
-            acc[t] = fmaf(r.y, v.y, acc[t]);
-            acc[t] = fmaf(r.z, v.z, acc[t]);
-            acc[t] = fmaf(r.w, v.w, acc[t]);
+            const float4* x4 = reinterpret_cast<const float4*>(P.x + size_t(t) * P.hidden) + k0;
+            float4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = k0 + j * n < h4 ? __ldg(x4 + j * n) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[t] = fmaf(r[j].x, v[j].x, acc[t]);
+              acc[t] = fmaf(r[j].y, v[j].y, acc[t]);
+              acc[t] = fmaf(r[j].z, v[j].z, acc[t]);
+              acc[t] = fmaf(r[j].w, v[j].w, acc[t]);
+              const uint32_t m = 0x7fffffffu;  // as integers, so that a NaN is the largest
+              most[t] = max(most[t], max(max(__float_as_uint(v[j].x) & m, __float_as_uint(v[j].y) & m),
+                                         max(__float_as_uint(v[j].z) & m, __float_as_uint(v[j].w) & m)));
+            }
           }
       }
 #pragma unroll
       for (int t = 0; t < kMlMaxTokens; ++t)
         if (t < P.tokens) {
           const float s = warp_sum(acc[t]);
-          if (lane == 0) S.red[warp][t] = s;
+          const uint32_t m = __reduce_max_sync(0xffffffffu, most[t]);
+          if (lane == 0) {
+            S.red[warp][t] = s;
+            atomicMax(&S.xmax[t], m);
+          }
         }
       ml_consumers_sync();
-      if (tid < P.tokens) {
-        float s = 0.f;
-        for (int w = 0; w < kMlWarps; ++w) s += S.red[w][tid];
-        P.logits[size_t(tid) * P.n_experts + e] = s;
+      if (warp < P.tokens) {
+        float s = lane < kMlWarps && (!two || lane < kMlWarps / 2) ? S.red[lane][warp] : 0.f;
+        float s1 = two && lane < kMlWarps / 2 ? S.red[kMlWarps / 2 + lane][warp] : 0.f;
+        s = warp_sum(s);
+        s1 = warp_sum(s1);
+        if (lane == 0) {
+          if (b < P.n_experts) P.logits[size_t(warp) * P.n_experts + b] = s;
+          if (two) P.logits[size_t(warp) * P.n_experts + b + G] = s1;
+        }
+        if (P.tokens > 1) asm volatile("bar.sync 2, %0;" ::"r"(32 * P.tokens) : "memory");
+        else __syncwarp();
+        if (P.x_smem && tid == 0) ml_arrive(P.bar);
       }
-      ml_consumers_sync();
+    }
+    // x in integer form: the CTA's own copy, or its share of the copy in global memory
+    const int x_row = 3 * ml_plane(P.hidden);
+    for (int s = 0; s < P.x_sets; ++s) {
+      uint8_t* dst = P.x_smem ? rec_s + s * P.tokens * x_row : P.xrec[s];
+      for (int i = P.x_smem ? tid : b * kMlConsumers + tid; i < P.tokens * (P.hidden / 16);
+           i += P.x_smem ? kMlConsumers : G * kMlConsumers)
+        ml_convert(P.x, P.hidden, S.xmax, P.set_order[s], dst, i);
     }
     ml_consumers_sync();
-    if (tid == 0) ml_arrive(P.bar);
+    if (!P.x_smem && tid == 0) ml_arrive(P.bar);
     if (P.tokens > 1 && warp < P.tokens) {
       bool ok = true;
       if (lane == 0) ok = ml_wait(P.bar, uint32_t(G));
@@ -627,207 +813,191 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     bool ok = true, listed = false;
     auto need_list = [&]() {
       if (!listed) {
-        ok = mbar_wait(&S.list_ready, 0) && !*(volatile int*)&S.abort;
+        ml_list_sync();
+        ok = ok && !*(volatile int*)&S.abort;
         listed = true;
       }
       return ok;
     };
-    if (!P.x_smem) need_list();  // the records in global memory are complete behind barrier 1
+    if (!P.x_smem) {  // the rows in global memory are complete behind barrier 1
+      if (tid == 0 && !ml_wait(P.bar, uint32_t(G))) *(volatile int*)&S.abort = 1;
+      ml_consumers_sync();
+      ok = !*(volatile int*)&S.abort;
+    }
 
     const uint32_t ring_s = smem_u32(smem);
-    MlX X;
-    const uint8_t* held = nullptr;
-    // Slice j of item i.  The item is in its slot once the slot's sequence number says so, and only
-    // then does the parity of `full` tell the item's own phase.
-    auto run_item = [&](int i, int j) -> bool {
-      const int slot = i % P.slots;
-      int seq;
-      const unsigned long long t0 = globaltimer_ns();
-      for (;;) {
-        asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(seq) : "r"(smem_u32(&S.seq[slot])) : "memory");
-        if (seq == i) break;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-          flag_error(BQG_DEVERR_TIMEOUT);
-          return false;
-        }
-        __nanosleep(40);
-      }
-      if (!mbar_wait(&S.full[slot], uint32_t(i / P.slots) & 1u)) return false;
-      const int4 d = ld_desc(&S.desc[slot][0]), o = ld_desc(&S.desc[slot][1]);
-      const uint32_t at = ring_s + uint32_t(slot) * P.slot_bytes;
-      const int fam = d.x & 1;
-      const bool first = d.x < 2;
+    const int g = lane >> 2, q = lane & 3;
+    // Passes: phase 1 shared, routed, phase 2 shared, routed.  In each, the warps form groups of as
+    // many warps as an item has tiles x parts; a group takes every groups-th item, a warp always the
+    // same tile and part.
+    int done_items = 0;
+    for (int pass = P.has_shared ? 0 : 1; pass < 4; ++pass) {
+      if (pass == 2 && !P.has_shared) continue;
+      const bool first = pass < 2;
+      const int fam = pass & 1 ? 0 : 1;
       const MlFam& F = P.fam[fam];
-      const int slices = first ? P.slices : F.slices;
-      const uint32_t m0 = fam ? (1u << P.tokens) - 1u : S.act_mask[d.y][0], m1 = fam ? 0u : S.act_mask[d.y][1];
+      if (pass == 1) need_list();
+      const int i0 = done_items;
+      if (first) done_items = fam ? ml_dealt(n_shared) : S.n1;
+      else done_items += (fam ? 1 : S.n_active) * ml_div_up(rows, F.nr);
+      const int parts = first ? F.parts1 : F.parts2, size = first ? parts : parts * F.tiles, groups = kMlWarps / size;
+      const int grp = warp / size, unit = warp - grp * size, j = unit % parts, tile = 8 * (unit / parts);
+      const int fmt = F.fmt, cols = first ? P.hidden : F.inter, rb = first ? F.rb1 : F.rb2, units = cols / 32;
+      const int steps = ml_steps(fmt, cols), s0 = steps * j / parts, s1 = steps * (j + 1) / parts;
+      const int plane = ml_plane(cols);
+      const bool in_smem = first ? P.x_smem : P.h_smem;
       const uint8_t* recs;
-      float* out;
-      int pair_step, n_units, per_token;
-      if (first) {
-        const int s = F.x_order;
-        int f0, f1;
-        ml_features(F.inter, fam ? 0 : d.y, f0, f1);
-        recs = P.x_smem ? rec_s + size_t(s) * P.tokens * units * kMlRecBytes : P.xrec[s];
-        n_units = units;
-        pair_step = F.share * 2 * slices;
-        out = sums + (fam ? size_t(pairs) * P.fam[0].share * 2 * slices : 0) + (d.z - f0) * 2 * slices;
-        per_token = fam ? 1 : P.top_k;
-      } else {
-        recs = P.h_smem ? rec_s + (fam ? size_t(pairs) * (P.fam[0].inter / 32) * kMlRecBytes : 0) : P.hrec[fam];
-        n_units = F.inter / 32;
-        pair_step = P.rows_cta * slices;
-        out = sums + (fam ? size_t(pairs) * P.rows_cta * P.fam[0].slices : 0) + (d.z - hr0) * slices;
-        per_token = 1;
+      if (first) recs = in_smem ? rec_s + F.x_set * P.tokens * x_row : P.xrec[F.x_set];
+      else recs = in_smem ? rec_s + (fam ? pairs * 3 * ml_plane(P.fam[0].inter) : 0) : P.hrec[fam];
+      // the column's plane (column 3 repeats the high digits) and the lane's part of a step
+      const uint64_t rec0 = (in_smem ? uint64_t(smem_u32(recs)) : reinterpret_cast<uint64_t>(recs)) +
+                            uint32_t(min(g & 3, 2) * plane + (ml_rowwise(fmt) ? 32 : 8) * q);
+      const float form = fmt == BQG_Q8_0 ? 1.f : fmt == BQG_I2_ROW ? 1.f / 64.f : 1.f / 16.f;
+      const int fam_pairs = fam ? pairs : 0;
+      // `done` counts all the warps: the groups' number for each of the item's warps, the first one the rest
+      const int count = groups + (unit == 0 ? kMlWarps - size * groups : 0);
+      for (int i = grp < groups ? i0 + grp : done_items; i < done_items && ok; i += groups) {
+        const int slot = i % kMlSlots;
+        if (!ml_wait_seq(&S.seq[slot], i)) {
+          ok = false;
+          break;
+        }
+        const int4 d = ld_desc(&S.desc[slot][0]), o = ld_desc(&S.desc[slot][1]);
+        const int np = d.w;
+        // The lane's two rows, row tile + g of either block.  Odd g take them the other way round: with
+        // the second block half of 128 bytes further, the rows that one wavefront reads fall into
+        // different banks.
+        const int t0 = min(tile + g, o.z - 1), t1 = min(tile + g, (o.w > 0 ? o.w : o.z) - 1);
+        float rs0 = 1.f, rs1 = 1.f;
+        if (ml_rowwise(fmt)) {
+          const int4 at = ld_desc(&S.desc[slot][2]);
+          rs0 = __ldg(reinterpret_cast<const float*>(uint64_t(uint32_t(at.x)) | uint64_t(uint32_t(at.y)) << 32) + t0);
+          if (o.w > 0) rs1 = __ldg(reinterpret_cast<const float*>(uint64_t(uint32_t(at.z)) | uint64_t(uint32_t(at.w)) << 32) + t1);
+        }
+        const uint32_t b0 = ring_s + uint32_t(o.x + t0 * rb), b1 = ring_s + uint32_t(o.y + t1 * rb);
+        const uint32_t a0 = g & 1 ? b1 : b0, a1 = g & 1 ? b0 : b1;
+        if (!mbar_wait(&S.full[slot], uint32_t(i / kMlSlots) & 1u)) {
+          ok = false;
+          break;
+        }
+        for (int k = 0; k < np; k += 2) {
+          // the column's pair (past the item's last: that one again)
+          const int p = S.order[d.z + min(k + (g >> 2), np - 1)];
+          const uint64_t bb = rec0 + uint32_t((first ? p >> 8 : (p & 255) - fam_pairs) * 3 * plane);
+          const bool has_b = k + (g >> 2) < np;
+          float v[2];
+          auto run = [&](auto fmt_c) {
+            if (in_smem) ml_tile<decltype(fmt_c)::value, true>(a0, a1, bb, has_b, units, s0, s1, v);
+            else ml_tile<decltype(fmt_c)::value, false>(a0, a1, bb, has_b, units, s0, s1, v);
+          };
+          switch (fmt) {
+            case BQG_Q8_0: run(MlInt<BQG_Q8_0>{}); break;
+            case BQG_Q4_0: run(MlInt<BQG_Q4_0>{}); break;
+            case BQG_I4_ROW: run(MlInt<BQG_I4_ROW>{}); break;
+            default: run(MlInt<BQG_I2_ROW>{});
+          }
+          const int kk = k + (q >> 1);
+          if (!(q & 1) && kk < np) {
+            const float y0 = (g & 1 ? v[1] : v[0]) * (rs0 * form), y1 = (g & 1 ? v[0] : v[1]) * (rs1 * form);
+            if (first) {
+              float* out = sums + ((slot * P.parts_max + j) * P.tokens + kk) * 16 + g;
+              out[0] = y0;
+              out[8] = y1;
+            } else {
+              const int pair = (S.order[d.z + kk] & 255) - fam_pairs;
+              float* out = y_sums + F.y_first + pair * F.y_step + j * P.rows_cta + (d.x - hr0) + tile + g;
+              if (tile + g < o.z) out[0] = y0;
+              if (tile + g < o.w) out[o.z] = y1;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&S.done[slot])), "r"(count)
+                       : "memory");
       }
-      const uint32_t up = first ? uint32_t(o.y - o.x) : 0u;
-      const int rb = first ? F.rb1 : F.rb2;
-      switch (F.fmt) {
-        case BQG_Q8_0:
-          ml_item<BQG_Q8_0>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
-          break;
-        case BQG_Q4_0:
-          ml_item<BQG_Q4_0>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
-          break;
-        case BQG_I4_ROW:
-          ml_item<BQG_I4_ROW>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
-          break;
-        default:
-          ml_item<BQG_I2_ROW>(at + o.x, up, rb, d.w, n_units, slices, j, m0, m1, per_token, recs, out, pair_step, X, held);
-      }
-      __syncwarp();
-      if (lane == 0)  // the slot is free when all its slices are done
-        asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&S.empty[slot])),
-                     "r"(j == 0 ? kMlArrivals - (slices - 1) : 1)
-                     : "memory");
-      return true;
-    };
+      if (pass != 1) continue;
 
-    // phase 1: warp = (group, slice); group g takes items g, g + groups, ..., so that a warp stays on
-    // its slice of x
-    {
-      const int groups = kMlWarps / P.slices;
-      if (warp < groups * P.slices) {
-        const int j = warp % P.slices;
-        for (int i = warp / P.slices; ok; i += groups) {
-          if (i >= S.n_shared1 && (!need_list() || i >= S.n1)) break;
-          if (!run_item(i, j)) ok = false;
-        }
-      }
-    }
-    if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
-    need_list();
-    ml_consumers_sync();
-    // h = act(g) u of the CTA's features, the slices added in order
-    if (!*(volatile int*)&S.abort) {
-      const int n0 = pairs * P.fam[0].share, n = n0 + (P.has_shared ? P.tokens * P.fam[1].share : 0);
-      for (int i = tid; i < n; i += kMlConsumers) {
-        const int fam = i >= n0 ? 1 : 0;
-        const MlFam& F = P.fam[fam];
-        const int p = (i - fam * n0) / F.share, f = (i - fam * n0) - p * F.share;
-        int f0, f1;
-        ml_features(F.inter, fam ? 0 : S.pair_a[p], f0, f1);
-        if (f0 + f >= f1) continue;
-        const float* s = sums + size_t(i) * 2 * P.slices;
-        float g = 0.f, u = 0.f;
-        for (int j = 0; j < P.slices; ++j) {
-          g += s[j];
-          u += s[P.slices + j];
-        }
-        const long long e = fam ? 0 : S.sel_e[p];
-        g *= ml_scale(F.fmt, F.gate + e * F.gate_stride + F.off1, f0 + f);
-        u *= ml_scale(F.fmt, F.up + e * F.up_stride + F.off1, f0 + f);
-        P.h[fam][size_t(p) * F.inter + f0 + f] = act_fn(P.act, g) * u;
-      }
-    }
-    ml_consumers_sync();
-    // grid barrier 2: every h is written
-    if (tid == 0) {
-      ml_arrive(P.bar + kMlBar);
-      if (*(volatile int*)&S.abort || !ml_wait(P.bar + kMlBar, uint32_t(G))) *(volatile int*)&S.abort = 1;
-    }
-    ml_consumers_sync();
-    if (!*(volatile int*)&S.abort) {
-      const int iu = P.fam[0].inter / 32;
-      const int i0 = P.h_smem ? tid : b * kMlConsumers + tid, step = P.h_smem ? kMlConsumers : G * kMlConsumers;
-      ml_convert(P.h[0], pairs * iu, ml_order(P.fam[0].fmt), P.h_smem ? rec_s : P.hrec[0], i0, step);
-      if (P.has_shared)
-        ml_convert(P.h[1], P.tokens * (P.fam[1].inter / 32), ml_order(P.fam[1].fmt),
-                   P.h_smem ? rec_s + size_t(pairs) * iu * kMlRecBytes : P.hrec[1], i0, step);
-    }
-    ml_consumers_sync();
-    if (!P.h_smem) {
+      // between the phases: grid barrier 2 (every h is written), h in integer form
+      if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
+      ml_consumers_sync();
       if (tid == 0) {
-        ml_arrive(P.bar + 2 * kMlBar);
-        if (*(volatile int*)&S.abort || !ml_wait(P.bar + 2 * kMlBar, uint32_t(G))) *(volatile int*)&S.abort = 1;
+        if (!mbar_wait(&S.h_ready, 0)) *(volatile int*)&S.abort = 1;
+        ml_arrive(P.bar + kMlBar);
+        if (*(volatile int*)&S.abort || !ml_wait(P.bar + kMlBar, uint32_t(G))) *(volatile int*)&S.abort = 1;
       }
       ml_consumers_sync();
-    }
-    // phase 2: a warp claims slices of items
-    ok = !*(volatile int*)&S.abort;
-    held = nullptr;
-    {
-      const int rows = hr1 - hr0;
-      const int si = P.has_shared ? ml_div_up(rows, P.fam[1].nr) : 0, st = si * P.fam[1].slices;
-      while (ok) {
-        int t = 0;
-        if (lane == 0) t = atomicAdd(&S.next, 1);
-        t = __shfl_sync(0xffffffffu, t, 0);
-        if (t >= S.tasks2) break;
-        const int fam = t < st ? 1 : 0;
-        const int in = t - (fam ? 0 : st), slices = P.fam[fam].slices;
-        if (!run_item(S.n1 + (fam ? 0 : si) + in / slices, in % slices)) ok = false;
+      if (!*(volatile int*)&S.abort) {
+        for (int r = tid; r < pairs + P.tokens; r += kMlConsumers) S.hmax[r] = __ldcg(P.bar + kMlHmax + r);
+        const int n0 = pairs * (P.fam[0].inter / 16), n = n0 + (P.has_shared ? P.tokens * (P.fam[1].inter / 16) : 0);
+        for (int i = P.h_smem ? tid : b * kMlConsumers + tid; i < n; i += P.h_smem ? kMlConsumers : G * kMlConsumers) {
+          const int f = i >= n0 ? 1 : 0;
+          uint8_t* dst = P.h_smem ? rec_s + (f ? pairs * 3 * ml_plane(P.fam[0].inter) : 0) : P.hrec[f];
+          ml_convert(P.h[f], P.fam[f].inter, P.bar + kMlHmax + (f ? pairs : 0), ml_order(P.fam[f].fmt), dst, i - f * n0);
+        }
       }
+      ml_consumers_sync();
+      if (!P.h_smem) {
+        if (tid == 0) {
+          ml_arrive(P.bar + 2 * kMlBar);
+          if (*(volatile int*)&S.abort || !ml_wait(P.bar + 2 * kMlBar, uint32_t(G))) *(volatile int*)&S.abort = 1;
+        }
+        ml_consumers_sync();
+      }
+      ok = ok && !*(volatile int*)&S.abort;
     }
     if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
     ml_consumers_sync();
+    // y: the parts of a pair's row added in order, then the pairs in slot order
     if (!*(volatile int*)&S.abort) {
-      const int rows = hr1 - hr0, sl0 = P.fam[0].slices, sl1 = P.fam[1].slices;
+      const int all = pairs + (P.has_shared ? P.tokens : 0);
+      for (int i = tid; i < all * rows; i += kMlConsumers) {
+        const int p = i / rows, r = i - p * rows, fam = p >= pairs ? 1 : 0;
+        const MlFam& F = P.fam[fam];
+        float* at = y_sums + F.y_first + (p - (fam ? pairs : 0)) * F.y_step + r;
+        float v = 0.f;
+#pragma unroll 2
+        for (int c = 0; c < F.parts2; ++c) v += at[c * P.rows_cta];
+        at[0] = v * ml_row_scale(S.hmax[p]) * (fam ? 1.f : S.sel_w[p]);
+      }
+    }
+    ml_consumers_sync();
+    if (!*(volatile int*)&S.abort)
       for (int i = tid; i < P.tokens * rows; i += kMlConsumers) {
         const int t = i / rows, r = i - t * rows;
         float acc = 0.f;
-        for (int q = 0; q < P.top_k; ++q) {
-          const int p = t * P.top_k + q;
-          const float* s = sums + (size_t(p) * P.rows_cta + r) * sl0;
-          float v = 0.f;
-          for (int j = 0; j < sl0; ++j) v += s[j];
-          v *= ml_scale(P.fam[0].fmt, P.fam[0].down + (long long)S.sel_e[p] * P.fam[0].down_stride + P.fam[0].off2, hr0 + r);
-          acc = fmaf(S.sel_w[p], v, acc);
-        }
-        if (P.has_shared) {
-          const float* s = sums + size_t(pairs) * P.rows_cta * sl0 + (size_t(t) * P.rows_cta + r) * sl1;
-          float v = 0.f;
-          for (int j = 0; j < sl1; ++j) v += s[j];
-          acc += v * ml_scale(P.fam[1].fmt, P.fam[1].down + P.fam[1].off2, hr0 + r);
-        }
+#pragma unroll 2
+        for (int k = 0; k < P.top_k; ++k) acc += y_sums[(t * P.top_k + k) * P.fam[0].y_step + r];
+        if (P.has_shared) acc += y_sums[P.fam[1].y_first + t * P.fam[1].y_step + r];
         P.y[size_t(t) * P.hidden + hr0 + r] = acc;
       }
-    }
   }
   __syncthreads();
-  // The last CTA to leave clears the counters: nobody waits on them any more.
+  // The last CTA to leave clears the state: nobody waits on it any more.
   if (threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(P.bar + 3 * kMlBar, 1u) == uint32_t(G) - 1u) {
       for (int i = 0; i < 4; ++i) P.bar[i * kMlBar] = 0u;
+      for (int i = 0; i < pairs + P.tokens; ++i) P.bar[kMlHmax + i] = 0u;
     }
   }
 }
 
 // ---------------------------------------------------------------- host side
-static_assert(4 * kMlBar * sizeof(uint32_t) <= BQG_MOE_LAYER_STATE_BYTES, "barrier counters");
+static_assert((kMlHmax + kMlMaxPairs + kMlMaxTokens) * sizeof(uint32_t) <= BQG_MOE_LAYER_STATE_BYTES, "barriers and max|h|");
+
+constexpr size_t kMlXCap = 100 * 1024;   // digit rows kept in shared memory (the ring needs the rest)
+constexpr size_t kMlHCap = 80 * 1024;
+constexpr size_t kMlSmem = 227 * 1024 - sizeof(MlShared) - 1024;
+constexpr int kMlItem = 56 * 1024;       // most bytes of an item
 
 struct MlLayout {
-  size_t bar, logits, h[2], xrec[2], hrec[2], sums, total;
-  int x_sets, set_order[2], x_order[2], x_smem, h_smem, sums_smem;
-  size_t rec_bytes, sums_cta;
+  size_t bar, logits, h[2], xrec[2], hrec[2], total;
+  int x_sets, set_order[2], x_set[2], x_smem, h_smem;
+  size_t rec_bytes;
 };
-constexpr size_t kMlRecCap = 64 * 1024;  // records kept in shared memory (the ring needs the rest)
-constexpr size_t kMlSumCap = 32 * 1024;  // partial sums kept in shared memory
-constexpr size_t kMlSmem = 227 * 1024 - sizeof(MlShared) - 1024;
 
-inline int ml_slices(int cols) { return (cols / 32 + 31) / 32; }
-
-inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens, int grid) {
+inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens) {
   MlLayout o{};
   const bool sh = L->s_gate != nullptr;
   const size_t T = size_t(tokens), pairs = T * L->top_k;
@@ -837,45 +1007,37 @@ inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens, int grid) {
     off = align256(off + bytes);
     return at;
   };
-  o.bar = take(4 * kMlBar * sizeof(uint32_t));
+  o.bar = take(BQG_MOE_LAYER_STATE_BYTES);
   o.logits = take(4 * T * L->n_experts);
   o.h[0] = take(4 * pairs * L->inter);
   o.h[1] = sh ? take(4 * T * L->shared_inter) : 0;
   o.set_order[0] = ml_order(L->expert_fmt);
   o.x_sets = 1;
   if (sh && ml_order(L->shared_fmt) != o.set_order[0]) {
-    o.x_order[1] = 1;
+    o.x_set[1] = 1;
     o.set_order[1] = ml_order(L->shared_fmt);
     o.x_sets = 2;
   }
-  const size_t xb = T * (L->hidden / 32) * kMlRecBytes;
-  const size_t hb0 = pairs * (L->inter / 32) * kMlRecBytes, hb1 = sh ? T * (L->shared_inter / 32) * kMlRecBytes : 0;
-  o.x_smem = xb * o.x_sets <= kMlRecCap;
-  o.h_smem = hb0 + hb1 <= kMlRecCap;
+  // 128 bytes more: the last step of a row may read past its last unit
+  const size_t xb = T * 3 * ml_plane(L->hidden);
+  const size_t hb0 = pairs * 3 * ml_plane(L->inter), hb1 = sh ? T * 3 * ml_plane(L->shared_inter) : 0;
+  o.x_smem = xb * o.x_sets <= kMlXCap;
+  o.h_smem = hb0 + hb1 <= kMlHCap;
   if (!o.x_smem)
-    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb);
+    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb + 128);
   if (!o.h_smem) {
-    o.hrec[0] = take(hb0);
-    o.hrec[1] = sh ? take(hb1) : 0;
+    o.hrec[0] = take(hb0 + 128);
+    o.hrec[1] = sh ? take(hb1 + 128) : 0;
   }
   if (o.x_smem) o.rec_bytes = xb * o.x_sets;
   if (o.h_smem && hb0 + hb1 > o.rec_bytes) o.rec_bytes = hb0 + hb1;
-  // partial sums of a CTA: the larger of the two phases'
-  auto up = [&](int n) { return size_t((n + grid - 1) / grid); };
-  const size_t s1 = 2 * size_t(ml_slices(L->hidden)) * (pairs * up(L->inter) + (sh ? T * up(L->shared_inter) : 0));
-  const size_t s2 = up(L->hidden) * (pairs * ml_slices(L->inter) + (sh ? T * ml_slices(L->shared_inter) : 0));
-  o.sums_cta = s1 > s2 ? s1 : s2;
-  o.sums_smem = 4 * o.sums_cta <= kMlSumCap;
-  if (!o.sums_smem) o.sums = take(4 * o.sums_cta * grid);
+  o.rec_bytes = (o.rec_bytes + 128 + 127) / 128 * 128;
   o.total = off;
   return o;
 }
 
-// Rows per item: the CTA's share of an expert in equal pieces of at most about kMlItem bytes, so that
-// a warp's slice of x serves many rows and the ring still holds several items.
-constexpr int kMlItem = 24 * 1024;
 inline MlFam ml_fam(int fmt, int hidden, int inter, const void* gate, const void* up, const void* down, size_t gs,
-                    size_t us, size_t ds, int x_order, int grid) {
+                    size_t us, size_t ds, int x_set, int grid, int most) {
   MlFam F{};
   F.gate = static_cast<const uint8_t*>(gate);
   F.up = static_cast<const uint8_t*>(up);
@@ -887,26 +1049,36 @@ inline MlFam ml_fam(int fmt, int hidden, int inter, const void* gate, const void
   F.inter = inter;
   F.rb1 = mg_row_bytes(fmt, hidden);
   F.rb2 = mg_row_bytes(fmt, inter);
-  if (fmt == BQG_I4_ROW || fmt == BQG_I2_ROW) {
+  if (ml_rowwise(fmt)) {
     F.off1 = int((size_t(inter) * F.rb1 + 15) / 16 * 16);
     F.off2 = int((size_t(hidden) * F.rb2 + 15) / 16 * 16);
   }
-  auto pieces = [](int n, long long bytes) {  // n rows of `bytes` in equal pieces
-    const long long most = kMlItem / bytes < 1 ? 1 : kMlItem / bytes;
-    const long long k = (n + most - 1) / most;
-    return int((n + k - 1) / k);
-  };
-  F.share = (inter + grid - 1) / grid;
-  F.nf = pieces(F.share, 2 * F.rb1);
-  F.nr = pieces((hidden + grid - 1) / grid, F.rb2);
-  F.slices = ml_slices(inter);
-  F.second = (F.nf * F.rb1 + 32 + 15) / 16 * 16;
-  F.x_order = x_order;
+  F.nf = 8;
+  while (F.nf > 1 && 2 * F.nf * F.rb1 > most) F.nf /= 2;
+  // half of 128 bytes past a multiple of 128
+  auto place = [](int bytes) { return (bytes + 30 + 63) / 128 * 128 + 64; };
+  F.second1 = place(F.nf * F.rb1);
+  F.items = inter / F.nf;
+  const int rows = (hidden + grid - 1) / grid;
+  int per = most / F.rb2;
+  if (per > 64) per = 64;
+  const int pieces = (rows + per - 1) / per;
+  F.nr = (rows + pieces - 1) / pieces;
+  F.tiles = ((F.nr + 1) / 2 + 7) / 8;
+  F.second2 = place((F.nr + 1) / 2 * F.rb2);
+  F.x_set = x_set;
   return F;
 }
-inline int ml_slot(const MlFam& F) {
-  const int a = 2 * F.second, b = (F.nr * F.rb2 + 32 + 15) / 16 * 16;
-  return ((a > b ? a : b) + 127) / 128 * 128;
+
+// Parts of an item's k range: several steps each,
+// so that a warp's fixed cost per part stays small, but enough of them for all warps when the CTA has
+// few items.
+inline int ml_parts(int fmt, int cols, int tiles, int items_cta, int most) {
+  const int steps = ml_steps(fmt, cols);
+  int best = 1;
+  for (int n = 2; n <= most && n <= steps; ++n)
+    if (n * tiles <= kMlWarps && (steps / n >= (ml_rowwise(fmt) ? 8 : 6) || items_cta * best * tiles < kMlWarps)) best = n;
+  return best;
 }
 
 inline SmemAttrOnce g_ml_attr;
@@ -915,7 +1087,7 @@ inline SmemAttrOnce g_ml_attr;
 
 extern "C" size_t moe_layer_workspace_size(const bqg_moe_layer* L, int tokens) {
   if (bqg::check_layer(L) != BQG_OK || tokens < 1 || tokens > bqg::kMlMaxTokens) return 0;
-  return bqg::ml_layout(L, tokens, bqg::kMlGrid).total;
+  return bqg::ml_layout(L, tokens).total;
 }
 
 extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x, float* y, int32_t* idx, float* w,
@@ -926,7 +1098,7 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   if (R == nullptr || x == nullptr || y == nullptr || tokens < 1 || (idx == nullptr) != (w == nullptr)) return BQG_ERR_ARG;
   if (tokens > kMlMaxTokens) return BQG_ERR_LIMIT;
   if (!aligned(R, 16) || !aligned(x, 16) || !aligned(y, 4) || !aligned(idx, 4) || !aligned(w, 4)) return BQG_ERR_ALIGN;
-  const MlLayout lay = ml_layout(L, tokens, kMlGrid);
+  const MlLayout lay = ml_layout(L, tokens);
   if (workspace == nullptr || ws_bytes < lay.total) return BQG_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return BQG_ERR_ALIGN;
   int dev;
@@ -936,12 +1108,34 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   if (info->sm_count < kMlGrid) return BQG_ERR_DEVICE;  // part of a GPU: its CTAs could not all be resident
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool sh = L->s_gate != nullptr;
+  const int pairs = tokens * L->top_k, touched = pairs < L->n_experts ? pairs : L->n_experts;
 
   MlParams P{};
+  P.rows_cta = (L->hidden + kMlGrid - 1) / kMlGrid;
+  P.parts_max = tokens <= 2 ? 12 : tokens <= 4 ? 8 : 4;  // the sums of a part take 64 bytes a token
+  const int parts2_max = tokens <= 2 ? 8 : tokens <= 4 ? 4 : 2;
+  const size_t sum_bytes = size_t(kMlSlots) * P.parts_max * tokens * 64;
+  const size_t y_bytes = (size_t(pairs + (sh ? tokens : 0)) * parts2_max * P.rows_cta * 4 + 127) / 128 * 128;
+  P.ring_bytes = int((kMlSmem - lay.rec_bytes - sum_bytes - y_bytes) / 128 * 128);
+  P.rec_off = P.ring_bytes;
+  P.sum_off = P.rec_off + int(lay.rec_bytes);
+  P.y_off = P.sum_off + int(sum_bytes);
+  const size_t smem = size_t(P.y_off) + y_bytes;
+  // at least three items in the ring
+  const int most = P.ring_bytes / 3 - 256 < kMlItem ? P.ring_bytes / 3 - 256 : kMlItem;
   P.fam[0] = ml_fam(L->expert_fmt, L->hidden, L->inter, L->gate, L->up, L->down, L->gate_stride, L->up_stride,
-                    L->down_stride, 0, kMlGrid);
-  P.fam[1] = sh ? ml_fam(L->shared_fmt, L->hidden, L->shared_inter, L->s_gate, L->s_up, L->s_down, 0, 0, 0, lay.x_order[1], kMlGrid)
+                    L->down_stride, 0, kMlGrid, most);
+  P.fam[1] = sh ? ml_fam(L->shared_fmt, L->hidden, L->shared_inter, L->s_gate, L->s_up, L->s_down, 0, 0, 0, lay.x_set[1], kMlGrid, most)
                 : P.fam[0];
+  auto up = [](int a, int b) { return (a + b - 1) / b; };
+  const int items1 = up((sh ? P.fam[1].items : 0) + touched * P.fam[0].items, kMlGrid);
+  const int items2 = (sh ? up(P.rows_cta, P.fam[1].nr) : 0) + touched * up(P.rows_cta, P.fam[0].nr);
+  for (MlFam& F : P.fam) {
+    F.parts1 = ml_parts(F.fmt, L->hidden, 1, items1, P.parts_max);
+    F.parts2 = ml_parts(F.fmt, F.inter, F.tiles, items2, parts2_max);
+    F.y_step = F.parts2 * P.rows_cta;
+  }
+  P.fam[1].y_first = pairs * P.fam[0].y_step;
   P.R = R;
   P.x = x;
   P.y = y;
@@ -964,21 +1158,6 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   P.x_sets = lay.x_sets;
   P.x_smem = lay.x_smem;
   P.h_smem = lay.h_smem;
-  P.slices = ml_slices(L->hidden);
-  P.sums = reinterpret_cast<float*>(ws + lay.sums);
-  P.sums_smem = lay.sums_smem;
-  P.sums_cta = int(lay.sums_cta);
-  P.rows_cta = (L->hidden + kMlGrid - 1) / kMlGrid;
-  const int s0 = ml_slot(P.fam[0]), s1 = ml_slot(P.fam[1]);
-  P.slot_bytes = s0 > s1 ? s0 : s1;
-  const size_t sum_bytes = lay.sums_smem ? (4 * lay.sums_cta + 127) / 128 * 128 : 0;
-  const size_t rec_bytes = (lay.rec_bytes + 127) / 128 * 128;
-  size_t slots = (kMlSmem - rec_bytes - sum_bytes) / size_t(P.slot_bytes);
-  if (slots > size_t(kMlMaxSlots)) slots = kMlMaxSlots;
-  P.slots = int(slots);
-  P.rec_off = P.slots * P.slot_bytes;
-  P.sum_off = P.rec_off + int(rec_bytes);
-  const size_t smem = size_t(P.sum_off) + sum_bytes;
   if ((st = g_ml_attr.ensure(dev, k_moe_layer, kMlSmem)) != BQG_OK) return st;
 
   // cooperative: the CTAs wait for one another, so all of them must be resident

@@ -316,7 +316,7 @@ BQG_API int moe_forward(const bqg_moe_layer* L, const float* x, const int32_t* i
  *   x and h are held as 24-bit fixed point per 32 values (|v - s V| <= about 2^-23 max|v|), so y is
  *   as exact as fp32 sums are; logits and weights are fp32.  Deterministic.  The kernel is a
  *   cooperative launch of one CTA per SM: it starts when every SM can take its CTA. */
-#define BQG_MOE_LAYER_STATE_BYTES 512
+#define BQG_MOE_LAYER_STATE_BYTES 1024
 BQG_API size_t moe_layer_workspace_size(const bqg_moe_layer* L, int tokens);
 BQG_API int moe_layer(const bqg_moe_layer* L, const float* R, const float* x, float* y, int32_t* idx, float* w,
                       int tokens, void* workspace, size_t ws_bytes, void* stream);
