@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t ml_pack(uint32_t a, uint32_t b, uint32_t c, 
 __device__ __forceinline__ void ml_digits(const float* src, const uint32_t* most, int order, uint8_t* row, int plane, int seg) {
   float4 v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(src) + i);
+  for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float4*>(src)[i];
   const float m = __uint_as_float(*(const volatile uint32_t*)most);
   const float inv = m > 1e-30f ? float(kMlDigitMax) / m : 0.f;  // below, Inf and NaN: zeros
   uint32_t t[16];
@@ -165,32 +165,42 @@ __host__ __device__ constexpr int ml_steps(int fmt, int cols) {
 // Steps [s0, s1) of 16 rows times two tokens.  a0, a1: shared-memory addresses of this lane's two
 // rows (tile rows lane / 4 and + 8); b: its column's digits, at its own part of a step.  out[0..1]:
 // the sums of the lane's rows for token (lane & 2) / 2, in units of the formats' byte forms (row
-// scales excluded); both lanes of a pair get them.  has_b: false in the lanes of a second token that is
-// not there, which load nothing (their columns are never used).
+// scales excluded); both lanes of a pair get them.
 template <int FMT, bool SM>
-__device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, bool has_b, int units, int s0, int s1,
-                                        float (&out)[2]) {
+__device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, int units, int s0, int s1, float (&out)[2]) {
   const int q = threadIdx.x & 3;
   const bool odd = q & 1;
   if constexpr (ml_rowwise(FMT)) {
     int c[2][4] = {};  // two chains of MMAs
-    uint4 x0 = {}, x1 = {};
     constexpr int kLane = FMT == BQG_I4_ROW ? 16 : 8;
     a0 += kLane * (4 * s0 + q);
     a1 += kLane * (4 * s0 + q);
     b += 128 * s0;
-#pragma unroll 2
-    for (int s = s0; s < s1; ++s) {
-      const bool in = 4 * s + q < units;  // past the row's end: zero weights
-      if (has_b) {
-        x0 = ml_ld128<SM>(b);
-        x1 = ml_ld128<SM>(b + 16);
+    struct Step {
+      uint4 v0, v1, x0, x1;
+    };
+    Step t[2] = {};
+    auto load = [&](Step& d) {
+      if constexpr (FMT == BQG_I4_ROW) {
+        d.v0 = lds128(a0);
+        d.v1 = lds128(a1);
+      } else {
+        const uint2 u0 = ml_ld64<true>(a0), u1 = ml_ld64<true>(a1);
+        d.v0.x = u0.x; d.v0.y = u0.y;
+        d.v1.x = u1.x; d.v1.y = u1.y;
       }
+      d.x0 = ml_ld128<SM>(b);
+      d.x1 = ml_ld128<SM>(b + 16);
+      a0 += 4 * kLane;
+      a1 += 4 * kLane;
+      b += 128;
+    };
+    auto step = [&](const Step& d, int s) {
+      const bool in = 4 * s + q < units;  // past the row's end: zero weights
       uint32_t w[4][4];                   // the MMAs' A registers
       if constexpr (FMT == BQG_I4_ROW) {
         const uint32_t keep = in ? 0xF0F0F0F0u : 0u;
-        const uint4 v0 = lds128(a0), v1 = lds128(a1);
-        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+        const uint32_t w0[4] = {d.v0.x, d.v0.y, d.v0.z, d.v0.w}, w1[4] = {d.v1.x, d.v1.y, d.v1.z, d.v1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           w[j][0] = (w0[j] << 4) & keep;
@@ -200,23 +210,29 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, bo
         }
       } else {
         const uint32_t keep = in ? 0xC0C0C0C0u : 0u;
-        const uint2 v0 = ml_ld64<true>(a0), v1 = ml_ld64<true>(a1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t w0 = j < 2 ? v0.x : v0.y, w1 = j < 2 ? v1.x : v1.y;
+          const uint32_t w0 = j < 2 ? d.v0.x : d.v0.y, w1 = j < 2 ? d.v1.x : d.v1.y;
           w[j][0] = (w0 << (j & 1 ? 2 : 6)) & keep;
           w[j][1] = (w1 << (j & 1 ? 2 : 6)) & keep;
           w[j][2] = (w0 << (j & 1 ? 0 : 4)) & keep;
           w[j][3] = (w1 << (j & 1 ? 0 : 4)) & keep;
         }
       }
-      ml_mma(c[0], w[0][0], w[0][1], w[0][2], w[0][3], x0.x, x0.y);
-      ml_mma(c[1], w[1][0], w[1][1], w[1][2], w[1][3], x0.z, x0.w);
-      ml_mma(c[0], w[2][0], w[2][1], w[2][2], w[2][3], x1.x, x1.y);
-      ml_mma(c[1], w[3][0], w[3][1], w[3][2], w[3][3], x1.z, x1.w);
-      a0 += 4 * kLane;
-      a1 += 4 * kLane;
-      b += 128;
+      ml_mma(c[0], w[0][0], w[0][1], w[0][2], w[0][3], d.x0.x, d.x0.y);
+      ml_mma(c[1], w[1][0], w[1][1], w[1][2], w[1][3], d.x0.z, d.x0.w);
+      ml_mma(c[0], w[2][0], w[2][1], w[2][2], w[2][3], d.x1.x, d.x1.y);
+      ml_mma(c[1], w[3][0], w[3][1], w[3][2], w[3][3], d.x1.z, d.x1.w);
+    };
+    // a step's loads before the MMAs of the step before it; the last one's are not used
+    load(t[0]);
+#pragma unroll 1
+    for (int s = s0; s < s1; s += 2) {
+      load(t[1]);
+      step(t[0], s);
+      if (s + 1 >= s1) break;
+      load(t[0]);
+      step(t[1], s + 1);
     }
     const float ma = odd ? 65536.f : 256.f, mb = odd ? 0.f : 1.f;
     out[0] = fmaf(float(c[0][0] + c[1][0]), ma, float(c[0][1] + c[1][1]) * mb);
@@ -235,10 +251,8 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, bo
     uint32_t e0[2] = {(a0 & ~3u) + 2 * r0 + 4 * q, (a0 & ~3u) + kUnit + 2 + 4 * q};
     uint32_t e1[2] = {(a1 & ~3u) + 2 * r1 + 4 * q, (a1 & ~3u) + kUnit + 2 + 4 * q};
     const uint32_t f0[2] = {16 - 8 * r0, 8 * r0}, f1[2] = {16 - 8 * r1, 8 * r1};
-    uint2 xs[2] = {};
     auto block = [&](int h) {
-      uint2& x = xs[h];
-      if (has_b) x = ml_ld64<SM>(b + 32 * h);
+      const uint2 x = ml_ld64<SM>(b + 32 * h);
       const uint32_t h0 = lds16(a0 + kUnit * h), h1 = lds16(a1 + kUnit * h);
       const uint32_t w0 = __funnelshift_r(lds32(e0[h]), lds32(e0[h] + 4), f0[h]);
       const uint32_t w1 = __funnelshift_r(lds32(e1[h]), lds32(e1[h] + 4), f1[h]);
@@ -510,123 +524,92 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     // ------------------------------------------------ producer
     const uint64_t pol = policy_evict_first();
     int i = 0, tail = 0, head = 0, oldest = 0;  // items [tail, i) hold the ring from `oldest` to `head`
-    bool ok = true;
-    int n1 = 1 << 30;  // items of phase 1, once known
-    // One copy of rows [r0, r0 + n) of a matrix to ring offset `at`: its 16-byte whole; the bytes past
-    // the matrix's last whole 16 by plain loads.
-    struct Copy {
-      uintptr_t from;
-      uint32_t bytes;
-      int off;
-    };
-    auto plan = [&](const uint8_t* base, int rb, int all, int r0, int n, int at) -> Copy {
-      const uintptr_t src = reinterpret_cast<uintptr_t>(base) + uint32_t(r0 * rb);
-      Copy c;
-      c.off = int(src & 15);
-      c.from = src - c.off;
-      c.bytes = uint32_t(c.off + n * rb + 15) & ~15u;
-      if (n == 0) {
-        c.bytes = 0;
-      } else if (r0 + n == all) {
-        const uint32_t whole = uint32_t(c.off + n * rb) & ~15u;
-#pragma unroll 1
-        for (uint32_t k = whole + lane; k < uint32_t(c.off + n * rb); k += 32) smem[at + k] = reinterpret_cast<const uint8_t*>(c.from)[k];
-        c.bytes = whole;
-      }
-      return c;
-    };
-    // An item is two blocks of rows: n of gate and of up, or the two halves of n rows of down.
-    auto put = [&](bool first, const MlFam& F, int e, int r0, int n, int p0, int np) -> bool {
-      const int rb = first ? F.rb1 : F.rb2, second = first ? F.second1 : F.second2;
-      const int na = first ? n : (n + 1) / 2, nb = n - (first ? 0 : na);
-      const int need = (second + nb * rb + 30 + 127) & ~127;
-      // a place; a full and a wrapped ring look alike: head <= oldest with items in it
-      for (;;) {
-        if (i == tail) head = oldest = 0;
-        if (i - tail < kMlSlots) {
-          const bool wrapped = i > tail && head <= oldest;
-          if (!wrapped && head + need > P.ring_bytes && need <= oldest) head = 0;
-          if (head + need <= (i > tail && head <= oldest ? oldest : P.ring_bytes)) break;
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(&S.done[tail % kMlSlots], uint32_t(tail / kMlSlots) & 1u))) return false;
-        ++tail;
-        if (tail < i) oldest = S.start[tail % kMlSlots];
-      }
-      // the slot's sums, where the helpers read them
-      const int last = i - kMlSlots;
-      if (last >= 0 && last < n1 &&
-          !__all_sync(0xffffffffu, mbar_wait(&S.empty[i % kMlSlots], uint32_t(last / kMlSlots) & 1u)))
-        return false;
-      fence_proxy_async_smem();
-      const int slot = i % kMlSlots;
-      uint64_t* bar = &S.full[slot];
-      const uint8_t* m0 = first ? F.gate + e * F.gate_stride : F.down + e * F.down_stride;
-      const uint8_t* m1 = first ? F.up + e * F.up_stride : m0;
-      const int all = first ? F.inter : P.hidden, r1 = first ? r0 : r0 + na;
-      const Copy c0 = plan(m0, rb, all, r0, na, head);
-      const Copy c1 = plan(m1, rb, all, r1, nb, head + second);
-      if (lane == 0) {
-        S.start[slot] = head;
-        S.desc[slot][0] = make_int4(r0, n, p0, np);
-        S.desc[slot][1] = make_int4(head + c0.off, nb > 0 ? head + second + c1.off : head + c0.off, na, nb);
-        if (ml_rowwise(F.fmt)) {  // where the rows' scales are
-          const int off = first ? F.off1 : F.off2;
-          const unsigned long long q0 = reinterpret_cast<unsigned long long>(m0) + uint32_t(off + 4 * r0);
-          const unsigned long long q1 = reinterpret_cast<unsigned long long>(m1) + uint32_t(off + 4 * r1);
-          S.desc[slot][2] = make_int4(int(q0), int(q0 >> 32), int(q1), int(q1 >> 32));
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&S.seq[slot])), "r"(i) : "memory");
-        if (c0.bytes + c1.bytes > 0) mbar_arrive_expect_tx(bar, c0.bytes + c1.bytes);
-        else mbar_arrive(bar);
-        if (c0.bytes) bulk_g2s(smem + head, reinterpret_cast<const void*>(c0.from), c0.bytes, bar, pol);
-        if (c1.bytes) bulk_g2s(smem + head + second, reinterpret_cast<const void*>(c1.from), c1.bytes, bar, pol);
-      }
-      head += need;
-      ++i;
-      return true;
-    };
-    // One call in a loop for all four kinds of items: phase 1 shared, routed, phase 2 shared, routed.
-    int id = b, active = 0;
-    bool listed = false;
+    int n1 = 1 << 30;                           // items of phase 1, once known
+    bool ok = true, listed = false;
+    // Passes: phase 1 shared, routed, phase 2 shared, routed.  A lane works out one item, up to 32 at a
+    // time, so that only the ring's bookkeeping and the copies are left between an item and the next
+    // (one after another: 0.9 us an item, the bound of the one-token layer).
     for (int pass = P.has_shared ? 0 : 1; pass < 4 && ok; ++pass) {
       if (pass == 1) {
         ml_list_sync();
         listed = true;
         ok = !*(volatile int*)&S.abort;
         if (!ok) break;
-        active = S.n_active;
         n1 = S.n1;
       }
       if (pass == 2 && !P.has_shared) continue;
-      const bool first = pass < 2;
-      const MlFam& F = P.fam[pass & 1 ? 0 : 1];
-      int a = 0, r = 0;
-      for (;;) {
-        int n = F.nf;
-        if (first) {
-          if (id >= n_shared + (pass == 1 ? active * F.items : 0)) break;
-          const int k = pass == 1 ? id - n_shared : id;
-          a = k / F.items;
-          r = (k - a * F.items) * F.nf;
-          id += G;
-        } else {
-          if (a >= (pass == 3 ? active : 1) || rows == 0) break;
-          n = min(F.nr, rows - r);
-        }
-        const bool routed = pass & 1;
-        const int p0 = routed ? S.act_first[a] : kMlMaxPairs;
-        ok = put(first, F, routed ? S.act_e[a] : 0, first ? r : hr0 + r, n, p0,
-                 routed ? S.act_first[a + 1] - p0 : P.tokens);
-        if (!ok) break;
-        if (!first) {
-          r += n;
-          if (r >= rows) {
-            r = 0;
-            ++a;
+      const bool first = pass < 2, routed = pass & 1;
+      const MlFam& F = P.fam[routed ? 0 : 1];
+      const int rb = first ? F.rb1 : F.rb2, all = first ? F.inter : P.hidden, second = first ? F.second1 : F.second2;
+      const int pieces = first ? F.items : ml_div_up(rows, F.nr), skip = first && routed ? n_shared : 0;
+      const int count = first ? (routed ? n1 : ml_dealt(n_shared)) - i : (routed ? S.n_active : 1) * pieces;
+      for (int t0 = 0; t0 < count && ok; t0 += 32) {
+        const int left = min(32, count - t0);
+        // an item: two blocks of rows, n of gate and of up, or the two halves of n rows of down
+        const int id = first ? b + (i + lane) * G - skip : t0 + lane;
+        const int a = lane < left ? id / pieces : 0, piece = lane < left ? id - a * pieces : 0;
+        const int r0 = first ? piece * F.nf : hr0 + piece * F.nr, n = first ? F.nf : min(F.nr, hr0 + rows - r0);
+        const int p0 = routed ? S.act_first[a] : kMlMaxPairs, np = routed ? S.act_first[a + 1] - p0 : P.tokens;
+        const int e = routed ? S.act_e[a] : 0;
+        const int na = first ? n : (n + 1) / 2, nb = n - (first ? 0 : na), r1 = first ? r0 : r0 + na;
+        const uint8_t* m0 = first ? F.gate + e * F.gate_stride : F.down + e * F.down_stride;
+        const uint8_t* m1 = first ? F.up + e * F.up_stride : m0;
+        const uintptr_t src0 = reinterpret_cast<uintptr_t>(m0) + uint32_t(r0 * rb);
+        const uintptr_t src1 = reinterpret_cast<uintptr_t>(m1) + uint32_t(r1 * rb);
+        const int off0 = int(src0 & 15), off1 = int(src1 & 15);
+        // whole 16 bytes; a matrix's last ones below them by plain loads
+        const bool last = r0 + n == all;
+        const int end0 = off0 + na * rb, end1 = off1 + nb * rb;
+        const bool last0 = last && (first || nb == 0), last1 = last && nb > 0;
+        const int bytes0 = (last0 ? end0 : end0 + 15) & ~15, bytes1 = nb == 0 ? 0 : (last1 ? end1 : end1 + 15) & ~15;
+        const int my_need = (second + nb * rb + 30 + 127) & ~127;
+        const int scales = first ? F.off1 : F.off2;
+        for (int l = 0; l < left; ++l, ++i) {
+          const int need = __shfl_sync(0xffffffffu, my_need, l), slot = i % kMlSlots;
+          // a place; a full and a wrapped ring look alike: head <= oldest with items in it
+          for (;;) {
+            if (i == tail) head = oldest = 0;
+            if (i - tail < kMlSlots) {
+              const bool wrapped = i > tail && head <= oldest;
+              if (!wrapped && head + need > P.ring_bytes && need <= oldest) head = 0;
+              if (head + need <= (i > tail && head <= oldest ? oldest : P.ring_bytes)) break;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.done[tail % kMlSlots], uint32_t(tail / kMlSlots) & 1u));
+            if (!ok) break;
+            ++tail;
+            if (tail < i) oldest = S.start[tail % kMlSlots];
           }
+          // the slot's sums, where the helpers read them
+          const int before = i - kMlSlots;
+          if (ok && before >= 0 && before < n1)
+            ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[slot], uint32_t(before / kMlSlots) & 1u));
+          if (!ok) break;
+          if (lane == l) {
+            fence_proxy_async_smem();
+            uint8_t* dst = smem + head;
+            if (last0)
+#pragma unroll 1
+              for (int k = bytes0; k < end0; ++k) dst[k] = reinterpret_cast<const uint8_t*>(src0 - off0)[k];
+            if (last1)
+#pragma unroll 1
+              for (int k = bytes1; k < end1; ++k) dst[second + k] = reinterpret_cast<const uint8_t*>(src1 - off1)[k];
+            S.start[slot] = head;
+            S.desc[slot][0] = make_int4(r0, n, p0, np);
+            S.desc[slot][1] = make_int4(head + off0, nb > 0 ? head + second + off1 : head + off0, na, nb);
+            if (ml_rowwise(F.fmt)) {  // where the rows' scales are
+              const unsigned long long q0 = reinterpret_cast<unsigned long long>(m0) + uint32_t(scales + 4 * r0);
+              const unsigned long long q1 = reinterpret_cast<unsigned long long>(m1) + uint32_t(scales + 4 * r1);
+              S.desc[slot][2] = make_int4(int(q0), int(q0 >> 32), int(q1), int(q1 >> 32));
+            }
+            asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(&S.seq[slot])), "r"(i) : "memory");
+            uint64_t* bar = &S.full[slot];
+            if (bytes0 + bytes1 > 0) mbar_arrive_expect_tx(bar, uint32_t(bytes0 + bytes1));
+            else mbar_arrive(bar);
+            if (bytes0) bulk_g2s(dst, reinterpret_cast<const void*>(src0 - off0), uint32_t(bytes0), bar, pol);
+            if (bytes1) bulk_g2s(dst + second, reinterpret_cast<const void*>(src1 - off1), uint32_t(bytes1), bar, pol);
+          }
+          __syncwarp();
+          head += need;
         }
       }
     }
@@ -642,6 +625,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     if (warp == kMlWarps + 1) {
       if (P.tokens == 1) {
         // twice: before the barrier on any numbers, which brings the code in from L2
+#pragma unroll 1
         for (int go = 0; go < 2; ++go) {
           if (go) {
             if (lane == 0) ok = ml_wait(P.bar, uint32_t(G));
@@ -884,11 +868,10 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
           // the column's pair (past the item's last: that one again)
           const int p = S.order[d.z + min(k + (g >> 2), np - 1)];
           const uint64_t bb = rec0 + uint32_t((first ? p >> 8 : (p & 255) - fam_pairs) * 3 * plane);
-          const bool has_b = k + (g >> 2) < np;
           float v[2];
           auto run = [&](auto fmt_c) {
-            if (in_smem) ml_tile<decltype(fmt_c)::value, true>(a0, a1, bb, has_b, units, s0, s1, v);
-            else ml_tile<decltype(fmt_c)::value, false>(a0, a1, bb, has_b, units, s0, s1, v);
+            if (in_smem) ml_tile<decltype(fmt_c)::value, true>(a0, a1, bb, units, s0, s1, v);
+            else ml_tile<decltype(fmt_c)::value, false>(a0, a1, bb, units, s0, s1, v);
           };
           switch (fmt) {
             case BQG_Q8_0: run(MlInt<BQG_Q8_0>{}); break;
@@ -930,7 +913,10 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       if (!*(volatile int*)&S.abort) {
         for (int r = tid; r < pairs + P.tokens; r += kMlConsumers) S.hmax[r] = __ldcg(P.bar + kMlHmax + r);
         const int n0 = pairs * (P.fam[0].inter / 16), n = n0 + (P.has_shared ? P.tokens * (P.fam[1].inter / 16) : 0);
-        for (int i = P.h_smem ? tid : b * kMlConsumers + tid; i < n; i += P.h_smem ? kMlConsumers : G * kMlConsumers) {
+        // own copies: every CTA starts elsewhere, so that they do not all ask L2 for the same lines
+        const int turn = P.h_smem ? int((long long)n * b / G) : 0;
+        for (int k = P.h_smem ? tid : b * kMlConsumers + tid; k < n; k += P.h_smem ? kMlConsumers : G * kMlConsumers) {
+          const int i = k + turn < n ? k + turn : k + turn - n;
           const int f = i >= n0 ? 1 : 0;
           uint8_t* dst = P.h_smem ? rec_s + (f ? pairs * 3 * ml_plane(P.fam[0].inter) : 0) : P.hrec[f];
           ml_convert(P.h[f], P.fam[f].inter, P.bar + kMlHmax + (f ? pairs : 0), ml_order(P.fam[f].fmt), dst, i - f * n0);
@@ -1018,20 +1004,20 @@ inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens) {
     o.set_order[1] = ml_order(L->shared_fmt);
     o.x_sets = 2;
   }
-  // 128 bytes more: the last step of a row may read past its last unit
+  // 384 bytes more: the last step of a row may read past its last unit, and one step ahead
   const size_t xb = T * 3 * ml_plane(L->hidden);
   const size_t hb0 = pairs * 3 * ml_plane(L->inter), hb1 = sh ? T * 3 * ml_plane(L->shared_inter) : 0;
   o.x_smem = xb * o.x_sets <= kMlXCap;
   o.h_smem = hb0 + hb1 <= kMlHCap;
   if (!o.x_smem)
-    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb + 128);
+    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb + 384);
   if (!o.h_smem) {
-    o.hrec[0] = take(hb0 + 128);
-    o.hrec[1] = sh ? take(hb1 + 128) : 0;
+    o.hrec[0] = take(hb0 + 384);
+    o.hrec[1] = sh ? take(hb1 + 384) : 0;
   }
   if (o.x_smem) o.rec_bytes = xb * o.x_sets;
   if (o.h_smem && hb0 + hb1 > o.rec_bytes) o.rec_bytes = hb0 + hb1;
-  o.rec_bytes = (o.rec_bytes + 128 + 127) / 128 * 128;
+  o.rec_bytes = (o.rec_bytes + 384 + 127) / 128 * 128;
   o.total = off;
   return o;
 }
