@@ -73,51 +73,60 @@ __host__ __device__ constexpr int ml_plane(int cols) { return cols + (48 - cols 
 __device__ __forceinline__ uint32_t ml_pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t sel) {
   return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
 }
-// 16 consecutive values (segment seg of a row) -> digits in the row's planes.
-__device__ __forceinline__ void ml_digits(const float* src, const uint32_t* most, int order, uint8_t* row, int plane, int seg) {
-  float4 v[4];
+// `rows` rows of `cols` fp32 values, row r's max|v| given by its bits in most[r] -> digit rows.  A lane takes four values at a time, i0, i0 + step, ... of all (a warp's lanes
+// are consecutive, and all of them call this); neighbours exchange bytes where a word's values are
+// apart.  Not inlined: x's call brings the code in for h's.
+__device__ __noinline__ void ml_convert(const float* src, int rows, int cols, const uint32_t* most, int order, uint8_t* dst,
+                                        int i0, int step) {
+  const int per = cols / 4, n = rows * per, plane = ml_plane(cols);
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll 1
+  for (int i = i0; (i & ~31) < n; i += 4 * step) {
+    float4 v[4];
+    int at[4];
+    float m[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float4*>(src)[i];
-  const float m = __uint_as_float(*(const volatile uint32_t*)most);
-  const float inv = m > 1e-30f ? float(kMlDigitMax) / m : 0.f;  // below, Inf and NaN: zeros
-  uint32_t t[16];
+    for (int u = 0; u < 4; ++u) {  // past the end: the last values, not stored
+      const int k = min(i + u * step, n - 1), r = k / per;
+      v[u] = reinterpret_cast<const float4*>(src)[k];
+      m[u] = __uint_as_float(most[r]);
+      int c = k - r * per;
+      if (order == kMlBytes) {  // words 0 .. 7 of a unit go to places 0, 2, 4, 6, 1, 3, 5, 7
+        const int w = c & 7;
+        c += (w < 4 ? 2 * w : 2 * w - 7) - w;
+      }
+      at[u] = r * 3 * plane + 4 * c;
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    for (int u = 0; u < 4; ++u) {
+      const int k = i + u * step;
+      if ((k & ~31) >= n) break;
+      const float inv = m[u] > 1e-30f ? float(kMlDigitMax) / m[u] : 0.f;  // below, Inf and NaN: zeros
+      const float f[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t t[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)  // adding 128 to every digit, with carries, and taking it off without
-      t[4 * i + j] = (uint32_t(__float2int_rn(f[j] * inv)) + 0x808080u) ^ 0x808080u;
-  }
+      for (int j = 0; j < 4; ++j)  // adding 128 to every digit, with carries, and taking it off without
+        t[j] = (uint32_t(__float2int_rn(f[j] * inv)) + 0x808080u) ^ 0x808080u;
 #pragma unroll
-  for (int p = 0; p < 3; ++p) {
-    const uint32_t sel = p == 0 ? 0x0051u : p == 1 ? 0x0040u : 0x0062u;
-    uint8_t* at = row + p * plane;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (order == kMlNibbles) {
-        const int o = 8 * (i >> 1) + (i & 1);
-        w[i] = ml_pack(t[o], t[o + 2], t[o + 4], t[o + 6], sel);
-      } else if (order == kMlPairs) {
-        w[i] = ml_pack(t[i], t[i + 4], t[i + 8], t[i + 12], sel);
-      } else {
-        w[i] = ml_pack(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3], sel);
+      for (int p = 0; p < 3; ++p) {
+        const uint32_t sel = p == 0 ? 0x0051u : p == 1 ? 0x0040u : 0x0062u;
+        uint32_t w;
+        if (order == kMlNibbles) {  // the even lane takes the pair's even values
+          const uint32_t mine = ml_pack(t[0], t[2], t[1], t[3], sel), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+          w = __byte_perm(mine, other, odd ? 0x3276 : 0x5410);
+        } else {
+          w = ml_pack(t[0], t[1], t[2], t[3], sel);
+          if (order == kMlPairs) {  // a 4 x 4 transpose over four lanes
+            uint32_t other = __shfl_xor_sync(0xffffffffu, w, 1);
+            w = __byte_perm(w, other, odd ? 0x3715 : 0x6240);
+            other = __shfl_xor_sync(0xffffffffu, w, 2);
+            w = __byte_perm(w, other, high ? 0x3276 : 0x5410);
+          }
+        }
+        if (k < n) *reinterpret_cast<uint32_t*>(dst + at[u] + p * plane) = w;
       }
     }
-    if (order == kMlBytes) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(at + 32 * (seg >> 1) + 8 * i + 4 * (seg & 1)) = w[i];
-    } else {
-      *reinterpret_cast<uint4*>(at + 16 * seg) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
   }
-}
-// `rows` rows of `cols` fp32 values, row r's max|v| given by its bits in most[r] (shared or global
-// memory) -> digit rows; segment i of all.  Not inlined: x's call brings the code in for h's.
-__device__ __noinline__ void ml_convert(const float* src, int cols, const uint32_t* most, int order, uint8_t* dst, int i) {
-  const int segs = cols / 16, plane = ml_plane(cols);
-  const int r = i / segs, s = i - r * segs;
-  ml_digits(src + size_t(i) * 16, most + r, order, dst + size_t(r) * 3 * plane, plane, s);
 }
 __device__ __forceinline__ float ml_row_scale(uint32_t most) { return __uint_as_float(most) * (1.f / float(kMlDigitMax)); }
 
@@ -317,7 +326,7 @@ struct MlParams {
   int tokens, n_experts, top_k, hidden, act, has_shared;
   // workspace
   uint32_t* bar;         // barrier counters, one per 128 bytes, and the rows' max|h|: zero between calls
-  float* logits;         // [tokens][n_experts]
+  float* logits;         // [tokens][BQG_MAX_EXPERTS]
   float* h[2];           // [pairs][inter], [tokens][shared inter]
   uint8_t* xrec[2];      // digit rows in global memory (when they do not fit shared memory)
   uint8_t* hrec[2];
@@ -394,17 +403,18 @@ __device__ __forceinline__ int ml_dealt(int n) {
 }
 
 // ---------------------------------------------------------------- selection of the experts
-// One warp, one token: the k largest logits (ties to the lower index; NaN below everything), and
+// One warp, one token: the k largest of a row of BQG_MAX_EXPERTS logits, the first E of them set (ties to the lower index; NaN below everything), and
 // weights e^(l - max) over the selected ones' sum, which is the renormalised softmax.
 __device__ __forceinline__ void ml_topk(const float* logits, int E, int k, int* sel_e, float* sel_w) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[8];  // increasing with the logit; 0: none or taken, 1: NaN
+  uint32_t key[8];  // of experts 8 lane ..; increasing with the logit; 0: none or taken, 1: NaN
+  float l[8];
+  *reinterpret_cast<float4*>(l) = __ldcg(reinterpret_cast<const float4*>(logits) + 2 * lane);
+  *reinterpret_cast<float4*>(l + 4) = __ldcg(reinterpret_cast<const float4*>(logits) + 2 * lane + 1);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int e = lane + 32 * i;
-    const float v = e < E ? __ldcg(logits + e) : 0.f;
-    const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);
-    key[i] = e >= E ? 0u : v != v ? 1u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(l[i] == 0.f ? 0.f : l[i]);
+    key[i] = 8 * lane + i >= E ? 0u : l[i] != l[i] ? 1u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
   }
   uint32_t mine = 1u;  // lane j keeps slot j
   int mine_e = 0;
@@ -419,10 +429,10 @@ __device__ __forceinline__ void ml_topk(const float* logits, int E, int k, int* 
         bi = i;
       }
     const uint32_t most = __reduce_max_sync(0xffffffffu, bk);
-    const unsigned e = __reduce_min_sync(0xffffffffu, bk == most ? unsigned(lane + 32 * bi) : 0x7fffffffu);
+    const unsigned e = __reduce_min_sync(0xffffffffu, bk == most ? unsigned(8 * lane + bi) : 0x7fffffffu);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (e == unsigned(lane + 32 * i)) key[i] = 0u;
+      if (e == unsigned(8 * lane + i)) key[i] = 0u;
     if (lane == j) {
       mine = most;
       mine_e = int(e);
@@ -630,9 +640,10 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
           if (go) {
             if (lane == 0) ok = ml_wait(P.bar, uint32_t(G));
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            __syncwarp();
           }
           if (ok) {
-            ml_topk(go ? P.logits : P.R, P.n_experts, P.top_k, S.sel_e, S.sel_w);
+            ml_topk(P.logits, P.n_experts, P.top_k, S.sel_e, S.sel_w);
             __syncwarp();
             ml_list(S, 1, P.top_k);
           }
@@ -729,21 +740,27 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       }
       for (int k0 = tid - grp * n; k0 < h4; k0 += 4 * n) {
         float4 r[4];
+        int at[4];  // past the row's end: its last values, not added (no branch: all loads in flight)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = has && k0 + j * n < h4 ? __ldg(r4 + k0 + j * n) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 4; ++j) {
+          at[j] = min(k0 + j * n, h4 - 1);
+          r[j] = __ldg(r4 + at[j]);
+        }
 #pragma unroll
         for (int t = 0; t < kMlMaxTokens; ++t)
           if (t < P.tokens) {
-            const float4* x4 = reinterpret_cast<const float4*>(P.x + size_t(t) * P.hidden) + k0;
+            const float4* x4 = reinterpret_cast<const float4*>(P.x + size_t(t) * P.hidden);
             float4 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = k0 + j * n < h4 ? __ldg(x4 + j * n) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < 4; ++j) v[j] = __ldg(x4 + at[j]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              acc[t] = fmaf(r[j].x, v[j].x, acc[t]);
-              acc[t] = fmaf(r[j].y, v[j].y, acc[t]);
-              acc[t] = fmaf(r[j].z, v[j].z, acc[t]);
-              acc[t] = fmaf(r[j].w, v[j].w, acc[t]);
+              float a = acc[t];
+              a = fmaf(r[j].x, v[j].x, a);
+              a = fmaf(r[j].y, v[j].y, a);
+              a = fmaf(r[j].z, v[j].z, a);
+              a = fmaf(r[j].w, v[j].w, a);
+              acc[t] = k0 + j * n < h4 ? a : acc[t];
               const uint32_t m = 0x7fffffffu;  // as integers, so that a NaN is the largest
               most[t] = max(most[t], max(max(__float_as_uint(v[j].x) & m, __float_as_uint(v[j].y) & m),
                                          max(__float_as_uint(v[j].z) & m, __float_as_uint(v[j].w) & m)));
@@ -767,8 +784,9 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         s = warp_sum(s);
         s1 = warp_sum(s1);
         if (lane == 0) {
-          if (b < P.n_experts) P.logits[size_t(warp) * P.n_experts + b] = s;
-          if (two) P.logits[size_t(warp) * P.n_experts + b + G] = s1;
+          float* at = P.logits + warp * BQG_MAX_EXPERTS + b;
+          if (b < P.n_experts) at[0] = s;
+          if (two) at[G] = s1;
         }
         if (P.tokens > 1) asm volatile("bar.sync 2, %0;" ::"r"(32 * P.tokens) : "memory");
         else __syncwarp();
@@ -777,19 +795,17 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     }
     // x in integer form: the CTA's own copy, or its share of the copy in global memory
     const int x_row = 3 * ml_plane(P.hidden);
-    for (int s = 0; s < P.x_sets; ++s) {
-      uint8_t* dst = P.x_smem ? rec_s + s * P.tokens * x_row : P.xrec[s];
-      for (int i = P.x_smem ? tid : b * kMlConsumers + tid; i < P.tokens * (P.hidden / 16);
-           i += P.x_smem ? kMlConsumers : G * kMlConsumers)
-        ml_convert(P.x, P.hidden, S.xmax, P.set_order[s], dst, i);
-    }
+    const int i0 = tid + (P.x_smem ? 0 : b * kMlConsumers), i_step = P.x_smem ? kMlConsumers : G * kMlConsumers;
+    for (int s = 0; s < P.x_sets; ++s)
+      ml_convert(P.x, P.tokens, P.hidden, S.xmax, P.set_order[s], P.x_smem ? rec_s + s * P.tokens * x_row : P.xrec[s], i0, i_step);
     ml_consumers_sync();
     if (!P.x_smem && tid == 0) ml_arrive(P.bar);
     if (P.tokens > 1 && warp < P.tokens) {
       bool ok = true;
       if (lane == 0) ok = ml_wait(P.bar, uint32_t(G));
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (ok) ml_topk(P.logits + size_t(warp) * P.n_experts, P.n_experts, P.top_k, S.sel_e + warp * P.top_k, S.sel_w + warp * P.top_k);
+      __syncwarp();
+      if (ok) ml_topk(P.logits + warp * BQG_MAX_EXPERTS, P.n_experts, P.top_k, S.sel_e + warp * P.top_k, S.sel_w + warp * P.top_k);
       else if (lane == 0) *(volatile int*)&S.abort = 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.topk_ready);
@@ -911,16 +927,13 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       }
       ml_consumers_sync();
       if (!*(volatile int*)&S.abort) {
-        for (int r = tid; r < pairs + P.tokens; r += kMlConsumers) S.hmax[r] = __ldcg(P.bar + kMlHmax + r);
-        const int n0 = pairs * (P.fam[0].inter / 16), n = n0 + (P.has_shared ? P.tokens * (P.fam[1].inter / 16) : 0);
-        // own copies: every CTA starts elsewhere, so that they do not all ask L2 for the same lines
-        const int turn = P.h_smem ? int((long long)n * b / G) : 0;
-        for (int k = P.h_smem ? tid : b * kMlConsumers + tid; k < n; k += P.h_smem ? kMlConsumers : G * kMlConsumers) {
-          const int i = k + turn < n ? k + turn : k + turn - n;
-          const int f = i >= n0 ? 1 : 0;
-          uint8_t* dst = P.h_smem ? rec_s + (f ? pairs * 3 * ml_plane(P.fam[0].inter) : 0) : P.hrec[f];
-          ml_convert(P.h[f], P.fam[f].inter, P.bar + kMlHmax + (f ? pairs : 0), ml_order(P.fam[f].fmt), dst, i - f * n0);
-        }
+        // once per CTA: a single line that 148 SMs ask for gives less than one answer a clock
+        if (tid < pairs + P.tokens) S.hmax[tid] = __ldcg(P.bar + kMlHmax + tid);
+        ml_consumers_sync();
+        const int c0 = tid + (P.h_smem ? 0 : b * kMlConsumers), step = P.h_smem ? kMlConsumers : G * kMlConsumers;
+        for (int f = 0; f <= P.has_shared; ++f)
+          ml_convert(P.h[f], f ? P.tokens : pairs, P.fam[f].inter, S.hmax + (f ? pairs : 0), ml_order(P.fam[f].fmt),
+                     P.h_smem ? rec_s + (f ? pairs * 3 * ml_plane(P.fam[0].inter) : 0) : P.hrec[f], c0, step);
       }
       ml_consumers_sync();
       if (!P.h_smem) {
@@ -994,7 +1007,7 @@ inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens) {
     return at;
   };
   o.bar = take(BQG_MOE_LAYER_STATE_BYTES);
-  o.logits = take(4 * T * L->n_experts);
+  o.logits = take(4 * T * BQG_MAX_EXPERTS);
   o.h[0] = take(4 * pairs * L->inter);
   o.h[1] = sh ? take(4 * T * L->shared_inter) : 0;
   o.set_order[0] = ml_order(L->expert_fmt);
