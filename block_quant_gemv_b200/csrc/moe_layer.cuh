@@ -185,26 +185,35 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, in
     a0 += kLane * (4 * s0 + q);
     a1 += kLane * (4 * s0 + q);
     b += 128 * s0;
-    struct Step {
-      uint4 v0, v1, x0, x1;
+    // Loads run ahead of the MMAs: the weights and digits in shared memory one step, digits in global
+    // memory (L2's latency) two; the last ones are not used.
+    constexpr int kAhead = SM ? 1 : 2, kStages = kAhead + 1;
+    struct Rows {
+      uint4 v0, v1;
     };
-    Step t[2] = {};
-    auto load = [&](Step& d) {
+    struct Digits {
+      uint4 x0, x1;
+    };
+    Rows r[kStages];
+    Digits x[kStages];
+    auto load_rows = [&](Rows& d) {
       if constexpr (FMT == BQG_I4_ROW) {
         d.v0 = lds128(a0);
         d.v1 = lds128(a1);
       } else {
         const uint2 u0 = ml_ld64<true>(a0), u1 = ml_ld64<true>(a1);
-        d.v0.x = u0.x; d.v0.y = u0.y;
-        d.v1.x = u1.x; d.v1.y = u1.y;
+        d.v0 = make_uint4(u0.x, u0.y, 0u, 0u);
+        d.v1 = make_uint4(u1.x, u1.y, 0u, 0u);
       }
-      d.x0 = ml_ld128<SM>(b);
-      d.x1 = ml_ld128<SM>(b + 16);
       a0 += 4 * kLane;
       a1 += 4 * kLane;
+    };
+    auto load_digits = [&](Digits& d) {
+      d.x0 = ml_ld128<SM>(b);
+      d.x1 = ml_ld128<SM>(b + 16);
       b += 128;
     };
-    auto step = [&](const Step& d, int s) {
+    auto step = [&](const Rows& d, const Digits& e, int s) {
       const bool in = 4 * s + q < units;  // past the row's end: zero weights
       uint32_t w[4][4];                   // the MMAs' A registers
       if constexpr (FMT == BQG_I4_ROW) {
@@ -228,20 +237,23 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, in
           w[j][3] = (w1 << (j & 1 ? 0 : 4)) & keep;
         }
       }
-      ml_mma(c[0], w[0][0], w[0][1], w[0][2], w[0][3], d.x0.x, d.x0.y);
-      ml_mma(c[1], w[1][0], w[1][1], w[1][2], w[1][3], d.x0.z, d.x0.w);
-      ml_mma(c[0], w[2][0], w[2][1], w[2][2], w[2][3], d.x1.x, d.x1.y);
-      ml_mma(c[1], w[3][0], w[3][1], w[3][2], w[3][3], d.x1.z, d.x1.w);
+      ml_mma(c[0], w[0][0], w[0][1], w[0][2], w[0][3], e.x0.x, e.x0.y);
+      ml_mma(c[1], w[1][0], w[1][1], w[1][2], w[1][3], e.x0.z, e.x0.w);
+      ml_mma(c[0], w[2][0], w[2][1], w[2][2], w[2][3], e.x1.x, e.x1.y);
+      ml_mma(c[1], w[3][0], w[3][1], w[3][2], w[3][3], e.x1.z, e.x1.w);
     };
-    // a step's loads before the MMAs of the step before it; the last one's are not used
-    load(t[0]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load_digits(x[k]);
+    load_rows(r[0]);
 #pragma unroll 1
-    for (int s = s0; s < s1; s += 2) {
-      load(t[1]);
-      step(t[0], s);
-      if (s + 1 >= s1) break;
-      load(t[0]);
-      step(t[1], s + 1);
+    for (int s = s0; s < s1; s += kStages) {
+#pragma unroll
+      for (int k = 0; k < kStages; ++k) {
+        if (s + k >= s1) break;
+        load_rows(r[(k + 1) % kStages]);
+        load_digits(x[(k + kAhead) % kStages]);
+        step(r[k], x[k], s + k);
+      }
     }
     const float ma = odd ? 65536.f : 256.f, mb = odd ? 0.f : 1.f;
     out[0] = fmaf(float(c[0][0] + c[1][0]), ma, float(c[0][1] + c[1][1]) * mb);
@@ -260,8 +272,14 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, in
     uint32_t e0[2] = {(a0 & ~3u) + 2 * r0 + 4 * q, (a0 & ~3u) + kUnit + 2 + 4 * q};
     uint32_t e1[2] = {(a1 & ~3u) + 2 * r1 + 4 * q, (a1 & ~3u) + kUnit + 2 + 4 * q};
     const uint32_t f0[2] = {16 - 8 * r0, 8 * r0}, f1[2] = {16 - 8 * r1, 8 * r1};
-    auto block = [&](int h) {
-      const uint2 x = ml_ld64<SM>(b + 32 * h);
+    constexpr int kAhead = SM ? 0 : 2, kStages = SM ? 2 : 3;  // steps that the digits are loaded ahead
+    uint2 xs[kStages][2];
+    auto load_digits = [&](uint2 (&d)[2]) {
+      d[0] = ml_ld64<SM>(b);
+      d[1] = ml_ld64<SM>(b + 32);
+      b += 64;
+    };
+    auto block = [&](int h, const uint2& x) {
       const uint32_t h0 = lds16(a0 + kUnit * h), h1 = lds16(a1 + kUnit * h);
       const uint32_t w0 = __funnelshift_r(lds32(e0[h]), lds32(e0[h] + 4), f0[h]);
       const uint32_t w1 = __funnelshift_r(lds32(e1[h]), lds32(e1[h] + 4), f1[h]);
@@ -278,18 +296,24 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, in
       acc[0] = fmaf(float(c[0] * mul + c[1]), half_bits_to_float(h0), acc[0]);
       acc[1] = fmaf(float(c[2] * mul + c[3]), half_bits_to_float(h1), acc[1]);
     };
-#pragma unroll 2
-    for (int s = s0; s < s1; ++s) {
-      block(0);
-      if (2 * s + 1 < units) block(1);
-      a0 += 2 * kUnit;
-      a1 += 2 * kUnit;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        e0[h] += 2 * kUnit;
-        e1[h] += 2 * kUnit;
+    for (int k = 0; k < kAhead; ++k) load_digits(xs[k]);
+#pragma unroll 1
+    for (int s = s0; s < s1; s += kStages) {
+#pragma unroll
+      for (int k = 0; k < kStages; ++k) {
+        if (s + k >= s1) break;
+        load_digits(xs[(k + kAhead) % kStages]);
+        block(0, xs[k][0]);
+        if (2 * (s + k) + 1 < units) block(1, xs[k][1]);
+        a0 += 2 * kUnit;
+        a1 += 2 * kUnit;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          e0[h] += 2 * kUnit;
+          e1[h] += 2 * kUnit;
+        }
       }
-      b += 64;
     }
     out[0] = acc[0] * (odd ? 256.f : 1.f);
     out[1] = acc[1] * (odd ? 256.f : 1.f);
@@ -1017,20 +1041,20 @@ inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens) {
     o.set_order[1] = ml_order(L->shared_fmt);
     o.x_sets = 2;
   }
-  // 384 bytes more: the last step of a row may read past its last unit, and one step ahead
+  // 640 bytes more: the last step of a row may read past its last unit, and the loads run two ahead
   const size_t xb = T * 3 * ml_plane(L->hidden);
   const size_t hb0 = pairs * 3 * ml_plane(L->inter), hb1 = sh ? T * 3 * ml_plane(L->shared_inter) : 0;
   o.x_smem = xb * o.x_sets <= kMlXCap;
   o.h_smem = hb0 + hb1 <= kMlHCap;
   if (!o.x_smem)
-    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb + 384);
+    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb + 640);
   if (!o.h_smem) {
-    o.hrec[0] = take(hb0 + 384);
-    o.hrec[1] = sh ? take(hb1 + 384) : 0;
+    o.hrec[0] = take(hb0 + 640);
+    o.hrec[1] = sh ? take(hb1 + 640) : 0;
   }
   if (o.x_smem) o.rec_bytes = xb * o.x_sets;
   if (o.h_smem && hb0 + hb1 > o.rec_bytes) o.rec_bytes = hb0 + hb1;
-  o.rec_bytes = (o.rec_bytes + 384 + 127) / 128 * 128;
+  o.rec_bytes = (o.rec_bytes + 640 + 127) / 128 * 128;
   o.total = off;
   return o;
 }
