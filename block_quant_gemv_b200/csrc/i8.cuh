@@ -334,6 +334,29 @@ __device__ __forceinline__ void it_store16h(const I8Params& P, const uint32_t (&
   }
 }
 
+// The tile's columns of one warp's 32 channels: scale, convert, store.
+__device__ __forceinline__ void it_store_tile(const I8Params& P, uint32_t lane_base, int columns, const float* sx, int t0,
+                                              int n, float sw, float bias, bool has_bias) {
+  const int ncol = min(columns, P.tokens - t0);
+#pragma unroll 1
+  for (int c = 0; c < ncol; c += 16) {
+    uint32_t v[16];
+    tmem_ld16(lane_base + uint32_t(c), v);
+    if (P.out == BQG_F32) {
+      if (n < P.n) {
+        float* y = static_cast<float*>(P.Y) + (long long)(t0 + c) * P.ldy + n;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (t0 + c + j < P.tokens) y[j * P.ldy] = i8_value(int(v[j]), sx[c + j], sw, bias, has_bias);
+      }
+    } else if (P.out == BQG_F16) {
+      it_store16h<__half>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
+    } else {
+      it_store16h<__nv_bfloat16>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
+    }
+  }
+}
+
 template <int BN>
 __global__ void __launch_bounds__(kItThreads, 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -461,24 +484,7 @@ __global__ void __launch_bounds__(kItThreads, 1)
       if (!mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u)) break;
       tc_fence_after();
       const uint32_t lane_base = tmem + uint32_t(buf * BN) + (uint32_t(quarter * 32) << 16);
-      const int ncol = min(BN, P.tokens - t0);
-#pragma unroll 1
-      for (int c = 0; c < ncol; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(lane_base + uint32_t(c), v);
-        if (P.out == BQG_F32) {
-          if (n < P.n) {
-            float* y = static_cast<float*>(P.Y) + (long long)(t0 + c) * P.ldy + n;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (t0 + c + j < P.tokens) y[j * P.ldy] = i8_value(int(v[j]), sx[c + j], sw, bias, has_bias);
-          }
-        } else if (P.out == BQG_F16) {
-          it_store16h<__half>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
-        } else {
-          it_store16h<__nv_bfloat16>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
-        }
-      }
+      it_store_tile(P, lane_base, BN, sx, t0, n, sw, bias, has_bias);
       tc_fence_before();
       mbar_arrive(&acc_empty[buf]);
     }
@@ -489,6 +495,188 @@ __global__ void __launch_bounds__(kItThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  }
+}
+
+// ---------------------------------------------------------------- large products: tiles of a CTA pair
+// One tile is 256 output channels x 256 tokens, computed by the two CTAs of a cluster (cta_group::2):
+// each holds 128 channels of W and 128 tokens of X in its shared memory and the sums of its channels in
+// its tensor memory; the first CTA issues M 256, N 256 MMAs that read both.  A CTA then loads 32 KB per
+// 128 k for the same MMAs that take 48 KB as a 128 x 256 tile of its own, whose 94 bytes a clock are
+// more than an SM gets from L2.  The warps' parts are k_i8_gemm's.
+constexpr int kI2M = 256, kI2N = 256, kI2Half = 128;
+constexpr int kI2StageBytes = 2 * kI2Half * kItK;
+constexpr int kI2Stages = 6;
+constexpr size_t kI2SmemBytes = 1024 + size_t(kI2Stages) * kI2StageBytes + 2 * 256 * sizeof(float) + 256;
+static_assert(kI2SmemBytes <= 227 * 1024, "int8 pair product shared memory");
+
+__device__ __forceinline__ void umma_i8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+// Arrives on `bar` of both CTAs once the MMAs issued so far have completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+// The first CTA's copy of a barrier.
+__device__ __forceinline__ uint32_t first_cta(uint64_t* bar) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
+}
+// A load into this CTA's shared memory whose bytes count on a barrier of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kItThreads, 1)
+    k_i8_gemm_pair(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                   const __grid_constant__ I8Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* a_ring = smem;
+  uint8_t* b_ring = a_ring + kI2Stages * kI2Half * kItK;
+  float* sx_s = reinterpret_cast<float*>(b_ring + kI2Stages * kI2Half * kItK);  // [2][256]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sx_s + 2 * 256);  // the first CTA's counts both CTAs' bytes
+  uint64_t* empty = full + kI2Stages;
+  uint64_t* acc_full = empty + kI2Stages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;      // [2], the first CTA's: 8 warps
+  uint64_t* done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  static_assert((2 * kI2Stages + 5) * 8 + 4 <= 256, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kI2Stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  const int ntn = (P.n + kI2M - 1) / kI2M, ntt = (P.tokens + kI2N - 1) / kI2N;
+  const long long tiles = (long long)ntn * ntt, pairs = gridDim.x / 2;
+  const int nk = (P.k + kItK - 1) / kItK;
+  auto place = [&](long long i, int& tn, int& tt) {  // as in k_i8_gemm
+    const long long per = (long long)kItRaster * ntn;
+    const int g = int(i / per);
+    const int w = min(kItRaster, ntt - g * kItRaster);
+    const int r = int(i - g * per);
+    tn = r / w;
+    tt = g * kItRaster + r - tn * w;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      long long s = 0;  // stages issued
+      bool ok = true;
+      for (long long i = blockIdx.x / 2; i < tiles && ok; i += pairs) {
+        int tn, tt;
+        place(i, tn, tt);
+        for (int kk = 0; kk < nk; ++kk, ++s) {
+          const int st = int(s % kI2Stages);
+          if (s >= kI2Stages && !mbar_wait(&empty[st], uint32_t(s / kI2Stages - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], uint32_t(2 * kI2StageBytes));
+          const uint32_t bar = first_cta(&full[st]);
+          tma_load_2d_pair(a_ring + st * kI2Half * kItK, &tmap_w, kk * kItK, tn * kI2M + rank * kI2Half, bar);
+          tma_load_2d_pair(b_ring + st * kI2Half * kItK, &tmap_x, kk * kItK, tt * kI2N + rank * kI2Half, bar);
+        }
+      }
+      if (!ok && rank == 0)  // bounded wait for the copies already issued, so none lands after the pair exits
+        for (long long q = (s > kI2Stages ? s - kI2Stages : 0); q < s; ++q)
+          mbar_wait(&full[q % kI2Stages], uint32_t(q / kI2Stages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      if (rank == 0) {
+        const uint32_t idesc = umma_idesc_s8(kI2M, kI2N);
+        long long s = 0;
+        int it = 0;
+        bool ok = true;
+        for (long long i = blockIdx.x / 2; i < tiles && ok; i += pairs, ++it) {
+          const int buf = it & 1;
+          if (it >= 2 && !mbar_wait(&acc_empty[buf], uint32_t(it / 2 - 1) & 1u)) break;
+          tc_fence_after();
+          const uint32_t acc = tmem + uint32_t(buf * kI2N);
+          for (int kk = 0; kk < nk; ++kk, ++s) {
+            const int st = int(s % kI2Stages);
+            if (!mbar_wait(&full[st], uint32_t(s / kI2Stages) & 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = smem_u32(a_ring + st * kI2Half * kItK), b = smem_u32(b_ring + st * kI2Half * kItK);
+#pragma unroll
+            for (int j = 0; j < kItK / 32; ++j)
+              umma_i8_pair(acc, umma_desc_sw128(a + 32 * j), umma_desc_sw128(b + 32 * j), idesc, (kk > 0 || j > 0) ? 1u : 0u);
+            umma_commit_pair(&empty[st]);
+          }
+          if (ok) umma_commit_pair(&acc_full[buf]);
+        }
+        umma_commit_pair(done);  // every MMA issued here has completed before tensor memory is freed
+      }
+      mbar_wait(done, 0);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const int et = int(threadIdx.x) - 64;  // 0..127
+    const bool has_bias = P.bias != nullptr;
+    int it = 0;
+    for (long long i = blockIdx.x / 2; i < tiles; i += pairs, ++it) {
+      const int buf = it & 1;
+      int tn, tt;
+      place(i, tn, tt);
+      const int n = tn * kI2M + rank * kI2Half + quarter * 32 + lane, t0 = tt * kI2N;
+      float* sx = sx_s + buf * 256;
+      for (int c = et; c < kI2N; c += 128) sx[c] = t0 + c < P.tokens ? __ldg(P.sx + t0 + c) : 0.f;
+      const float sw = n < P.n ? __ldg(P.sw + n) : 0.f;
+      const float bias = has_bias && n < P.n ? __ldg(P.bias + n) : 0.f;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (!mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u)) break;
+      tc_fence_after();
+      it_store_tile(P, tmem + uint32_t(buf * kI2N) + (uint32_t(quarter * 32) << 16), kI2N, sx, t0, n, sw, bias, has_bias);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_cta(&acc_empty[buf])) : "memory");
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA's memory is freed while the other still uses it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
 
@@ -523,7 +711,7 @@ inline bool i8_encode(CUtensorMap* m, const int8_t* p, size_t pitch, int rows, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline SmemAttrOnce g_i8_attr[5];
+inline SmemAttrOnce g_i8_attr[6];
 
 template <int BN>
 inline int launch_i8_gemm(const I8Params& P, int dev, const DeviceInfo* info, cudaStream_t s) {
@@ -538,8 +726,21 @@ inline int launch_i8_gemm(const I8Params& P, int dev, const DeviceInfo* info, cu
   return launch_pdl(k_i8_gemm<BN>, dim3(unsigned(grid)), dim3(kItThreads), it_smem_bytes(BN), s, tw, tx, P);
 }
 
+inline int launch_i8_gemm_pair(const I8Params& P, int dev, const DeviceInfo* info, cudaStream_t s) {
+  CUtensorMap tw, tx;
+  if (!i8_encode(&tw, P.W, size_t(P.ldw), P.n, P.k, kI2Half) || !i8_encode(&tx, P.X, size_t(P.ldx), P.tokens, P.k, kI2Half))
+    return BQG_ERR_CUDA;
+  const int st = g_i8_attr[5].ensure(dev, k_i8_gemm_pair, kI2SmemBytes);
+  if (st != BQG_OK) return st;
+  const long long tiles = (long long)((P.n + kI2M - 1) / kI2M) * ((P.tokens + kI2N - 1) / kI2N);
+  const int pairs = int(tiles < info->sm_count / 2 ? tiles : info->sm_count / 2);
+  return launch_pdl(k_i8_gemm_pair, dim3(unsigned(2 * pairs)), dim3(kItThreads), kI2SmemBytes, s, tw, tx, P);
+}
+
+constexpr int kI8Pair = 512;  // i8_tile_tokens: tiles of CTA pairs
 // Tokens per tile: the one whose waves of tiles take the least time, a tile's 128-k stage costing
-// the larger of its MMAs (2 BN cycles) and its bytes ((128 + BN) * 128 at ~64 bytes a cycle).
+// the larger of its MMAs (2 BN cycles) and its bytes ((128 + BN) * 128 at ~64 bytes a cycle; a pair's
+// tile 512 cycles of either).
 inline int i8_tile_tokens(int tokens, int n, int sms) {
   const int ntn = (n + kItM - 1) / kItM;
   int best = 16;
@@ -555,7 +756,9 @@ inline int i8_tile_tokens(int tokens, int n, int sms) {
     }
     if (bn >= tokens) break;
   }
-  return best;
+  const long long tiles = (long long)((n + kI2M - 1) / kI2M) * ((tokens + kI2N - 1) / kI2N);
+  const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
+  return waves * 512 < best_cost ? kI8Pair : best;
 }
 
 }  // namespace bqg
@@ -626,6 +829,7 @@ extern "C" int qgemm_i8(const int8_t* Xq, size_t ldx, const float* sx, const int
     case 32: return launch_i8_gemm<32>(P, dev, info, s);
     case 64: return launch_i8_gemm<64>(P, dev, info, s);
     case 128: return launch_i8_gemm<128>(P, dev, info, s);
-    default: return launch_i8_gemm<256>(P, dev, info, s);
+    case 256: return launch_i8_gemm<256>(P, dev, info, s);
+    default: return launch_i8_gemm_pair(P, dev, info, s);
   }
 }
