@@ -61,18 +61,22 @@ struct Elem<__nv_bfloat16> {
 };
 
 // ---------------------------------------------------------------- rows to int8
-// TPR threads own a row (32: 8 rows per CTA, 256: one row per CTA).  A thread keeps up to
-// kQrChunks chunks of 8 values in registers, so rows of up to TPR * 32 values are read once;
-// longer rows read the rest a second time (from L2).  Bytes bound it: 1 read and 1 write of the
-// row.
+// TPR threads own a row (32: 8 rows per CTA, else one row per CTA of TPR threads).  A thread keeps up
+// to kQrChunks chunks of 8 values in registers, so rows of up to TPR * 32 values are read once; longer
+// rows read the rest a second time (from L2).  Bytes bound it: 1 read and 1 write of the row; of the
+// TPR that hold a row, the smallest has the most bytes in flight (8192 x 4096 bf16: 256 threads a
+// row 40 us), the largest the shortest way for few rows.
 //
-// The rounding is decided exactly: with f = floor(x * (1 / s)) (off by at most one), q is f or
-// f + 1 by the sign of fma(-(f + 1/2), s, x), which is the sign of the exact difference (f + 1/2
-// has at most 9 bits; a fused result is 0 only for an exact tie, since s >= 2^-100 keeps it clear
-// of underflow).  A tie goes to the even integer.  A plain rint(x * (1 / s)) would miss borders:
-// bf16 rows meet exact ties often.
+// The rounding is decided exactly.  t = x * (1 / s) + 1.5 * 2^23 is rounded once, to a whole number
+// n (in t's low bits); x * (1 / s) is off from x / s by less than 127 * 2^-24 * 1.1, so wherever it
+// lies within 0.4999 of n, so does x / s within 1/2.  Otherwise, next to a border: with f = floor(x *
+// (1 / s)) (off by at most one), q is f or f + 1 by the sign of fma(-(f + 1/2), s, x), which is the
+// sign of the exact difference (f + 1/2 has at most 9 bits; a fused result is 0 only for an exact tie,
+// since s >= 2^-100 keeps it clear of underflow).  A tie goes to the even integer.  A plain rint(x *
+// (1 / s)) would miss borders: bf16 rows meet exact ties often.
 constexpr int kQrThreads = 256;
 constexpr int kQrChunks = 4;
+constexpr int kQrFewRows = 592;  // four rows an SM
 constexpr float kQrTinyScale = 7.888609052210118e-31f;  // 2^-100: a row below it is held as zeros
 
 __device__ __forceinline__ int round_quotient(float x, float s, float inv) {
@@ -83,11 +87,11 @@ __device__ __forceinline__ int round_quotient(float x, float s, float inv) {
 }
 
 template <typename T, int TPR, bool VEC>
-__global__ void __launch_bounds__(kQrThreads) k_quantize_rows(const T* __restrict__ X, long long ldx,
+__global__ void __launch_bounds__(TPR == 32 ? kQrThreads : TPR) k_quantize_rows(const T* __restrict__ X, long long ldx,
                                                               int8_t* __restrict__ Q, long long ldq,
                                                               float* __restrict__ scale, int rows, int k) {
-  constexpr int kRows = kQrThreads / TPR;
-  __shared__ uint32_t wmax[kQrThreads / 32];
+  constexpr int kRows = TPR == 32 ? kQrThreads / 32 : 1;
+  __shared__ uint32_t wmax[TPR / 32];
   griddep_launch_dependents();
   griddep_wait();
   const int tid = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kQrThreads) k_quantize_rows(const T* __restric
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = most;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQrThreads / 32; ++w) most = max(most, wmax[w]);
+    for (int w = 0; w < TPR / 32; ++w) most = max(most, wmax[w]);
   }
   float s = __fdiv_rn(__uint_as_float(most), 127.f);
   const bool finite = most < 0x7F800000u;
@@ -145,8 +149,22 @@ __global__ void __launch_bounds__(kQrThreads) k_quantize_rows(const T* __restric
   auto store = [&](int i0, const float (&v)[8]) {
     uint32_t w[2] = {0u, 0u};
     if (!zero) {
+      constexpr float kWhole = 12582912.f;  // 1.5 * 2^23
+      uint32_t b[8];
+      bool border = false;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t(round_quotient(v[j], s, inv)) & 0xFFu) << (8 * (j & 3));
+      for (int j = 0; j < 8; ++j) {
+        const float t = fmaf(v[j], inv, kWhole);
+        border |= fabsf(fmaf(v[j], inv, -(t - kWhole))) > 0.4999f;
+        b[j] = __float_as_uint(t);
+      }
+      if (border) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = uint32_t(round_quotient(v[j], s, inv));
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[j] = __byte_perm(__byte_perm(b[4 * j], b[4 * j + 1], 0x0040), __byte_perm(b[4 * j + 2], b[4 * j + 3], 0x0040), 0x5410);
     }
     if (i0 + 8 <= k) {
       *reinterpret_cast<uint2*>(q + i0) = make_uint2(w[0], w[1]);
@@ -505,6 +523,7 @@ __global__ void __launch_bounds__(kItThreads, 1)
 // 128 k for the same MMAs that take 48 KB as a 128 x 256 tile of its own, whose 94 bytes a clock are
 // more than an SM gets from L2.  The warps' parts are k_i8_gemm's.
 constexpr int kI2M = 256, kI2N = 256, kI2Half = 128;
+constexpr int kI2Threads = 320;  // 8 warps store: a quarter of the channels and half of the tokens each
 constexpr int kI2StageBytes = 2 * kI2Half * kItK;
 constexpr int kI2Stages = 6;
 constexpr size_t kI2SmemBytes = 1024 + size_t(kI2Stages) * kI2StageBytes + 2 * 256 * sizeof(float) + 256;
@@ -539,7 +558,7 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kItThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI2Threads, 1)
     k_i8_gemm_pair(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                    const __grid_constant__ I8Params P) {
   extern __shared__ uint8_t smem_raw[];
@@ -550,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kItThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sx_s + 2 * 256);  // the first CTA's counts both CTAs' bytes
   uint64_t* empty = full + kI2Stages;
   uint64_t* acc_full = empty + kI2Stages;  // [2]
-  uint64_t* acc_empty = acc_full + 2;      // [2], the first CTA's: 8 warps
+  uint64_t* acc_empty = acc_full + 2;      // [2], the first CTA's: both CTAs' storing warps
   uint64_t* done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   static_assert((2 * kI2Stages + 5) * 8 + 4 <= 256, "barrier area");
@@ -564,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kItThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], 16);
     }
     mbar_init(done, 1);
     fence_barrier_init();
@@ -648,8 +667,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kItThreads, 1)
       mbar_wait(done, 0);
     }
   } else {
-    const int quarter = warp & 3;
-    const int et = int(threadIdx.x) - 64;  // 0..127
+    const int quarter = warp & 3, col = (warp - 2) / 4 * kI2Half;
+    const int et = int(threadIdx.x) - 64;  // 0..255
     const bool has_bias = P.bias != nullptr;
     int it = 0;
     for (long long i = blockIdx.x / 2; i < tiles; i += pairs, ++it) {
@@ -658,13 +677,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kItThreads, 1)
       place(i, tn, tt);
       const int n = tn * kI2M + rank * kI2Half + quarter * 32 + lane, t0 = tt * kI2N;
       float* sx = sx_s + buf * 256;
-      for (int c = et; c < kI2N; c += 128) sx[c] = t0 + c < P.tokens ? __ldg(P.sx + t0 + c) : 0.f;
+      sx[et] = t0 + et < P.tokens ? __ldg(P.sx + t0 + et) : 0.f;
       const float sw = n < P.n ? __ldg(P.sw + n) : 0.f;
       const float bias = has_bias && n < P.n ? __ldg(P.bias + n) : 0.f;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u)) break;
       tc_fence_after();
-      it_store_tile(P, tmem + uint32_t(buf * kI2N) + (uint32_t(quarter * 32) << 16), kI2N, sx, t0, n, sw, bias, has_bias);
+      it_store_tile(P, tmem + uint32_t(buf * kI2N + col) + (uint32_t(quarter * 32) << 16), kI2Half, sx + col, t0 + col, n, sw,
+                    bias, has_bias);
       tc_fence_before();
       __syncwarp();
       if (lane == 0)
@@ -690,13 +710,19 @@ inline int launch_quantize_rows(const void* X, size_t ldx, int8_t* Q, size_t ldq
   const bool vec = aligned(X, 16) && ldx * sizeof(T) % 16 == 0;
   const T* x = static_cast<const T*>(X);
   const long long lx = (long long)ldx, lq = (long long)ldq;
-  if (k <= 32 * 8 * kQrChunks && rows > 1) {  // a warp per row: no barrier; with one row, all the threads
-    const unsigned grid = unsigned((rows + 7) / 8);
-    return vec ? launch_pdl(k_quantize_rows<T, 32, true>, dim3(grid), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k)
-               : launch_pdl(k_quantize_rows<T, 32, false>, dim3(grid), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k);
-  }
-  return vec ? launch_pdl(k_quantize_rows<T, 256, true>, dim3(unsigned(rows)), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k)
-             : launch_pdl(k_quantize_rows<T, 256, false>, dim3(unsigned(rows)), dim3(kQrThreads), 0, s, x, lx, Q, lq, scale, rows, k);
+  auto launch = [&](auto kernel, int tpr) {
+    const unsigned grid = tpr == 32 ? unsigned((rows + 7) / 8) : unsigned(rows);
+    return launch_pdl(kernel, dim3(grid), dim3(unsigned(tpr == 32 ? kQrThreads : tpr)), 0, s, x, lx, Q, lq, scale, rows, k);
+  };
+  // the smallest that keeps a row in registers; for one row and a few, as many threads as there are
+  constexpr int kHeld = 8 * kQrChunks;
+  if (k <= 32 * kHeld && rows > 1)
+    return vec ? launch(k_quantize_rows<T, 32, true>, 32) : launch(k_quantize_rows<T, 32, false>, 32);
+  if (k <= 64 * kHeld && rows > kQrFewRows)
+    return vec ? launch(k_quantize_rows<T, 64, true>, 64) : launch(k_quantize_rows<T, 64, false>, 64);
+  if (k <= 128 * kHeld && rows > kQrFewRows)
+    return vec ? launch(k_quantize_rows<T, 128, true>, 128) : launch(k_quantize_rows<T, 128, false>, 128);
+  return vec ? launch(k_quantize_rows<T, 256, true>, 256) : launch(k_quantize_rows<T, 256, false>, 256);
 }
 
 inline bool i8_encode(CUtensorMap* m, const int8_t* p, size_t pitch, int rows, int k, int box_rows) {
@@ -734,7 +760,7 @@ inline int launch_i8_gemm_pair(const I8Params& P, int dev, const DeviceInfo* inf
   if (st != BQG_OK) return st;
   const long long tiles = (long long)((P.n + kI2M - 1) / kI2M) * ((P.tokens + kI2N - 1) / kI2N);
   const int pairs = int(tiles < info->sm_count / 2 ? tiles : info->sm_count / 2);
-  return launch_pdl(k_i8_gemm_pair, dim3(unsigned(2 * pairs)), dim3(kItThreads), kI2SmemBytes, s, tw, tx, P);
+  return launch_pdl(k_i8_gemm_pair, dim3(unsigned(2 * pairs)), dim3(kI2Threads), kI2SmemBytes, s, tw, tx, P);
 }
 
 constexpr int kI8Pair = 512;  // i8_tile_tokens: tiles of CTA pairs
