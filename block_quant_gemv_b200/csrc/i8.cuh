@@ -21,24 +21,42 @@ namespace bqg {
 // ---------------------------------------------------------------- element types
 template <typename T>
 struct Elem;
+// Raw: eight values as they are stored.
 template <>
 struct Elem<float> {
-  static __device__ __forceinline__ float load(const float* p) { return *p; }
-  static __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  struct Raw {
+    uint32_t w[8];
+  };
+  static __device__ __forceinline__ Raw load8(const float* p) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+  }
+  static __device__ __forceinline__ void set(Raw& r, int i, float v) { r.w[i] = __float_as_uint(v); }
+  static __device__ __forceinline__ void values(const Raw& r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
   }
 };
+struct Raw16 {
+  uint32_t w[4];
+};
+template <typename T>
+__device__ __forceinline__ Raw16 load8_16(const T* p) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  return {{a.x, a.y, a.z, a.w}};
+}
+__device__ __forceinline__ void set16(Raw16& r, int i, uint32_t bits) {
+  r.w[i >> 1] = i & 1 ? (r.w[i >> 1] & 0xFFFFu) | bits << 16 : (r.w[i >> 1] & 0xFFFF0000u) | bits;
+}
 template <>
 struct Elem<__half> {
-  static __device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
-  static __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  using Raw = Raw16;
+  static __device__ __forceinline__ Raw load8(const __half* p) { return load8_16(p); }
+  static __device__ __forceinline__ void set(Raw& r, int i, __half v) { set16(r, i, __half_as_ushort(v)); }
+  static __device__ __forceinline__ void values(const Raw& r, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
       v[2 * i] = f.x;
       v[2 * i + 1] = f.y;
     }
@@ -47,14 +65,14 @@ struct Elem<__half> {
 };
 template <>
 struct Elem<__nv_bfloat16> {
-  static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  static __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  using Raw = Raw16;
+  static __device__ __forceinline__ Raw load8(const __nv_bfloat16* p) { return load8_16(p); }
+  static __device__ __forceinline__ void set(Raw& r, int i, __nv_bfloat16 v) { set16(r, i, __bfloat16_as_ushort(v)); }
+  static __device__ __forceinline__ void values(const Raw& r, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      v[2 * i] = __uint_as_float(r.w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
     }
   }
   static __device__ __forceinline__ uint32_t bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
@@ -101,37 +119,34 @@ __global__ void __launch_bounds__(TPR == 32 ? kQrThreads : TPR) k_quantize_rows(
   int8_t* q = Q + row * ldq;
   const int kmain = min(k, TPR * 8 * kQrChunks);
 
-  auto load = [&](int i0, float (&v)[8]) {  // values i0 .. i0 + 7 (0 past the row's end)
-    if (VEC && i0 + 8 <= k) {
-      Elem<T>::load8(x + i0, v);
-    } else {
+  using Raw = typename Elem<T>::Raw;
+  auto load = [&](int i0) -> Raw {  // values i0 .. i0 + 7 (0 past the row's end)
+    if (VEC && i0 + 8 <= k) return Elem<T>::load8(x + i0);
+    Raw r{};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = i0 + j < k ? Elem<T>::load(x + i0 + j) : 0.f;
-    }
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j < k) Elem<T>::set(r, j, x[i0 + j]);
+    return r;
   };
-  // |x| as an unsigned integer keeps the order and puts Inf and NaN above every finite value
-  uint32_t most = 0;
-  auto take = [&](const float (&v)[8]) {
+  float top = 0.f;  // max|x|, NaN if there is one
+  auto take = [&](const Raw& r) {
+    float v[8];
+    Elem<T>::values(r, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(v[j])));
   };
-  float keep[kQrChunks][8];
+  Raw keep[kQrChunks];
 #pragma unroll
   for (int c = 0; c < kQrChunks; ++c) {
     const int i0 = (c * TPR + tid) * 8;
-    if (i0 < kmain) load(i0, keep[c]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) keep[c][j] = 0.f;
+    keep[c] = Raw{};
+    if (i0 < kmain) keep[c] = load(i0);
   }
 #pragma unroll
   for (int c = 0; c < kQrChunks; ++c) take(keep[c]);
-  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) {
-    float v[8];
-    load(i0, v);
-    take(v);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
+  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) take(load(i0));
+  // as an unsigned integer, which keeps the order and puts Inf and NaN above every finite value
+  uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   if (TPR > 32) {
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = most;
     __syncthreads();
@@ -146,7 +161,9 @@ __global__ void __launch_bounds__(TPR == 32 ? kQrThreads : TPR) k_quantize_rows(
   const bool zero = !(s > 0.f);
   const float inv = zero ? 0.f : __fdiv_rn(1.f, s);
 
-  auto store = [&](int i0, const float (&v)[8]) {
+  auto store = [&](int i0, const Raw& r) {
+    float v[8];
+    Elem<T>::values(r, v);
     uint32_t w[2] = {0u, 0u};
     if (!zero) {
       constexpr float kWhole = 12582912.f;  // 1.5 * 2^23
@@ -177,11 +194,7 @@ __global__ void __launch_bounds__(TPR == 32 ? kQrThreads : TPR) k_quantize_rows(
     const int i0 = (c * TPR + tid) * 8;
     if (i0 < kmain) store(i0, keep[c]);
   }
-  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) {
-    float v[8];
-    load(i0, v);
-    store(i0, v);
-  }
+  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) store(i0, load(i0));
 }
 
 // ---------------------------------------------------------------- the product: arguments
