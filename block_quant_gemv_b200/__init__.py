@@ -290,7 +290,8 @@ def _row_pitch(name: str, t: torch.Tensor, dtypes, align: int) -> int:
 
 def _vector(name: str, t: torch.Tensor, n: int) -> int:
     """The address of a contiguous fp32 CUDA tensor of at least n values."""
-    _need_cuda(name, t, torch.float32)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.float32 and t.is_contiguous()):
+        _need_cuda(name, t, torch.float32)
     if t.numel() < n:
         raise ValueError(f"{name} must hold {n} values")
     return t.data_ptr()
@@ -302,7 +303,7 @@ def _call_on(fn, what: str, tensors, *args) -> None:
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"all tensors must be on one device: {tensors[0].device} and {t.device}")
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -318,16 +319,21 @@ def quantize_rows_i8(X: torch.Tensor, Xq: Optional[torch.Tensor] = None, scale: 
     ldx = _row_pitch("X", X, _TYPES, 1)
     rows, k = X.shape
     if Xq is None:
-        Xq = torch.empty(rows, (k + 15) // 16 * 16, dtype=torch.int8, device=X.device)
-        if k % 16:
+        ldq = (k + 15) // 16 * 16
+        Xq = torch.empty((rows, ldq), dtype=torch.int8, device=X.device)
+        if k != ldq:
             Xq = Xq[:, :k]
-    elif Xq.shape != X.shape:
-        raise ValueError(f"Xq must be {rows} x {k}")
+    else:
+        ldq = _row_pitch("Xq", Xq, (torch.int8,), 16)
+        if Xq.shape != X.shape:
+            raise ValueError(f"Xq must be {rows} x {k}")
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-    ldq = _row_pitch("Xq", Xq, (torch.int8,), 16)
+        scale = torch.empty((rows,), dtype=torch.float32, device=X.device)
+        at = scale.data_ptr()
+    else:
+        at = _vector("scale", scale, rows)
     _call_on(lib().quantize_rows_i8, "quantize_rows_i8", (X, Xq, scale), _TYPES[X.dtype], X.data_ptr(), ldx,
-             Xq.data_ptr(), ldq, _vector("scale", scale, rows), rows, k)
+             Xq.data_ptr(), ldq, at, rows, k)
     return Xq, scale
 
 
@@ -346,7 +352,7 @@ def qgemm_i8(Xq: torch.Tensor, sx: torch.Tensor, Wq: torch.Tensor, sw: torch.Ten
     if Y is None:
         if out_dtype not in _TYPES:
             raise TypeError(f"out_dtype must be {' or '.join(str(d) for d in _TYPES)}, got {out_dtype}")
-        Y = torch.empty(tokens, n, dtype=out_dtype, device=Xq.device)
+        Y = torch.empty((tokens, n), dtype=out_dtype, device=Xq.device)
         ldy = n
     else:
         ldy = _row_pitch("Y", Y, _TYPES, 1)
