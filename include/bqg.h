@@ -313,8 +313,8 @@ BQG_API int moe_forward(const bqg_moe_layer* L, const float* x, const int32_t* i
  *              first BQG_MOE_LAYER_STATE_BYTES once before the first call (cudaMemset); every call leaves
  *              them zero again, also one that set BQG_DEVERR_TIMEOUT.  The rest is scratch.  Calls
  *              that share a workspace must be ordered (one stream, or graphs replayed in order).
- *   x and h are held as 24-bit fixed point per 32 values (|v - s V| <= about 2^-23 max|v|), so y is
- *   as exact as fp32 sums are; logits and weights are fp32.  Deterministic.  The kernel is a
+ *   x and h are held as 24-bit fixed point per row (|v - s V| <= about 2^-24 max|row|), so y is as
+ *   exact as fp32 sums are, relative to max|y|; a row whose max|v| is below 1e-30 counts as zeros; logits and weights are fp32.  Deterministic.  The kernel is a
  *   cooperative launch of one CTA per SM: it starts when every SM can take its CTA. */
 #define BQG_MOE_LAYER_STATE_BYTES 1024
 BQG_API size_t moe_layer_workspace_size(const bqg_moe_layer* L, int tokens);
