@@ -82,8 +82,9 @@ struct Elem<__nv_bfloat16> {
 // TPR threads own a row (32: 8 rows per CTA, else one row per CTA of TPR threads).  A thread keeps up
 // to kQrChunks chunks of 8 values in registers, so rows of up to TPR * 32 values are read once; longer
 // rows read the rest a second time (from L2).  Bytes bound it: 1 read and 1 write of the row; of the
-// TPR that hold a row, the smallest has the most bytes in flight (8192 x 4096 bf16: 256 threads a
-// row 40 us), the largest the shortest way for few rows.
+// TPR that hold a row, the smallest has the most bytes in flight (8192 x 4096 bf16: 128 threads a row
+// 22.7 us; 256, and every rounding decided the long way, 40 us), the largest the shortest way for few
+// rows.  fp32 rows of 4096: 27.1 us, 6.2 TB/s.
 //
 // The rounding is decided exactly.  t = x * (1 / s) + 1.5 * 2^23 is rounded once, to a whole number
 // n (in t's low bits); x * (1 / s) is off from x / s by less than 127 * 2^-24 * 1.1, so wherever it
@@ -534,7 +535,9 @@ __global__ void __launch_bounds__(kItThreads, 1)
 // each holds 128 channels of W and 128 tokens of X in its shared memory and the sums of its channels in
 // its tensor memory; the first CTA issues M 256, N 256 MMAs that read both.  A CTA then loads 32 KB per
 // 128 k for the same MMAs that take 48 KB as a 128 x 256 tile of its own, whose 94 bytes a clock are
-// more than an SM gets from L2.  The warps' parts are k_i8_gemm's.
+// more than an SM gets from L2.  The warps' parts are k_i8_gemm's, but eight warps store.
+// 8192 tokens, k 4096, n 14336, bf16 out: 457 us as 128 x 256 tiles (2.1 POP/s), 435 us with four storing
+// warps (a tile's 256 columns took longer than its 32 stages), 308 us (3.1 POP/s; tensor pipe 82 % active).
 constexpr int kI2M = 256, kI2N = 256, kI2Half = 128;
 constexpr int kI2Threads = 320;  // 8 warps store: a quarter of the channels and half of the tokens each
 constexpr int kI2StageBytes = 2 * kI2Half * kItK;

@@ -15,28 +15,35 @@
 //      grid barrier 3)
 //   2  down: the CTA's share of the output rows, for every touched expert, so that the sum over
 //      experts stays in the CTA: y is written once, in slot order, with no further barrier.
-// One producer warp streams all the CTA's weights of both phases through one ring of bulk copies
-// and runs ahead of the barriers: the shared expert's rows load during phase 0, the down rows
-// during phase 1 and barrier 2.
+// Warps: 16 consumers; a producer that streams all the CTA's weights of both phases through one ring of
+// bulk copies and runs ahead of the barriers (the shared expert's rows load during phase 0, the down
+// rows during phase 1 and barrier 2); three helpers, the first of which selects the experts, that add an
+// item's parts, form h and its maximum.
 //
 // Products.  A warp multiplies a tile of 16 weight rows by up to 8 columns with the integer MMA of
 // the register file (m16n8k32): the weights become signed bytes in registers on their way from
 // shared memory, so nothing is written back, which operands in tensor memory or shared memory would
 // need, and at 8 columns the rate of the instruction is not the bound (0.49 a clock and SM measured:
-// a GLM-like layer's 302 M weights take 4 us).  The columns are the digits of x: x and h are 24-bit
-// fixed point per row, as three signed byte digits (256 m + l + 65536 h), and columns 4 t .. 4 t + 2
-// hold the middle, low and high digit of the group's token t (two tokens a pass).  All sums of a
-// block (Q8_0, Q4_0) or of the row (int4, int2) are exact integers; the only approximation is
-// |x - s X| <= about 2^-23 max|x|.  Nibble and 2-bit weights are taken as signed bytes in place (a
-// nibble in the high half of its byte is 16 q, a 2-bit code in the top bits 64 q; q - 8 of Q4_0 is
-// the two's-complement nibble u ^ 8): no offset corrections.
-// A dp4a per digit instead was bound by instructions (256-expert int4 layer: 76 us for one token,
-// 403 us for 8).
+// the 302 M weights of 8 experts of 3 x 2048 x 6144 take 4 us).  The columns are the digits of x: x
+// and h are 24-bit fixed point per row, as three signed byte digits (65536 h + 256 m + l), and columns
+// 4 t .. 4 t + 2 hold the middle, low and high digit of the group's token t (two tokens a pass).  All
+// sums of a block (Q8_0, Q4_0) or of a part of the row (int4, int2) are exact integers; the only
+// approximation is |x - s X| <= about 2^-24 max|row|.  Nibble and 2-bit weights are taken as signed
+// bytes in place (a nibble in the high half of its byte is 16 q, a 2-bit code in the top bits 64 q;
+// q - 8 of Q4_0 is the two's-complement nibble u ^ 8): no offset corrections.
 //
 // Work split.  Phase 1: items of up to 8 features (8 gate rows, the same 8 up rows: one tile) are
-// dealt out over the grid one by one.  Phase 2: the CTA's rows of one expert in tiles of up to 16.
-// An item's k range is cut into parts, one consumer warp each; the last part's warp adds the parts in
-// order.
+// dealt out over the grid one by one.  Phase 2: the CTA's rows of one expert, in tiles of up to 16.
+// A group of consumer warps takes an item, a warp one tile and one part of the k range; the parts are
+// added in order afterwards, so results do not depend on timing.
+//
+// Measured (us a call; weights' bytes at the HBM copy rate in brackets): 128 Q4_0 experts of 704 x 2816,
+// top 8, a shared Q8_0 expert of 2112: one token 34 [7], 5 tokens 96 [21]; 256 int4 experts of 2048 x
+// 6144, top 8: one token 44 [24], 8 tokens 265 [166].  One token: 18 us of the 44 (13 of a layer of 16
+// experts of 256 x 512, 15.5) remain with no items at all: launch, router, two grid barriers, h's way
+// through L2; with almost no MMAs it takes 42.  8 tokens: 198 with almost no MMAs, the rest is the
+// digits' way from L2 and the consumers.
+// dp4a, one per digit, in place of the MMA: 77 us and 410 us (256 experts, 1 and 8 tokens).
 #pragma once
 
 #include "common.cuh"
@@ -49,7 +56,7 @@ namespace bqg {
 constexpr int kMlGrid = 148;                       // CTAs: one per SM of a B200
 constexpr int kMlMaxTokens = BQG_MOE_LAYER_MAX_TOKENS;
 constexpr int kMlMaxPairs = kMlMaxTokens * BQG_MAX_TOPK;
-constexpr int kMlWarps = 16;                       // consumer warps
+constexpr int kMlWarps = 16;                       // consumer warps (24, at 72 registers: 42 us instead of 37)
 constexpr int kMlConsumers = 32 * kMlWarps;
 constexpr int kMlHelpers = 3;                      // warps that select the experts and finish h
 constexpr int kMlThreads = kMlConsumers + 32 + 32 * kMlHelpers;  // + producer warp
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     bool ok = true, listed = false;
     // Passes: phase 1 shared, routed, phase 2 shared, routed.  A lane works out one item, up to 32 at a
     // time, so that only the ring's bookkeeping and the copies are left between an item and the next
-    // (one after another: 0.9 us an item, the bound of the one-token layer).
+    // (one item after another: 0.9 us each, 47.6 us instead of 44.7).
     for (int pass = P.has_shared ? 0 : 1; pass < 4 && ok; ++pass) {
       if (pass == 1) {
         ml_list_sync();
@@ -1012,7 +1019,9 @@ static_assert((kMlHmax + kMlMaxPairs + kMlMaxTokens) * sizeof(uint32_t) <= BQG_M
 constexpr size_t kMlXCap = 100 * 1024;   // digit rows kept in shared memory (the ring needs the rest)
 constexpr size_t kMlHCap = 80 * 1024;
 constexpr size_t kMlSmem = 227 * 1024 - sizeof(MlShared) - 1024;
-constexpr int kMlItem = 56 * 1024;       // most bytes of an item
+// Most bytes of an item.  An item's tile takes the same MMAs however few its rows: with 28 KB the
+// 256-expert layer takes 58 us instead of 45 for one token.
+constexpr int kMlItem = 56 * 1024;
 
 struct MlLayout {
   size_t bar, logits, h[2], xrec[2], hrec[2], total;
