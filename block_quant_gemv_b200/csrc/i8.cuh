@@ -210,6 +210,7 @@ struct I8Params {
   int tokens, n, k;
   int out;   // BQG_F32, BQG_F16 or BQG_BF16
   int pair;  // 16-bit outputs: rows of Y are 4-byte aligned, two values per store
+  int split; // parts of k, CTAs of a cluster (k_i8_gemm<BN, true>)
 };
 
 __device__ __forceinline__ float i8_value(int sum, float sx, float sw, float bias, bool has_bias) {
@@ -337,14 +338,14 @@ __device__ __forceinline__ void umma_i8(uint32_t tmem_d, uint64_t adesc, uint64_
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
-// 16 accumulator columns (tokens t0 .. t0 + 15) of this lane's channel.
-template <typename T>
-__device__ __forceinline__ void it_store16h(const I8Params& P, const uint32_t (&v)[16], const float* sx, int t0, int n,
-                                            float sw, float bias, bool has_bias) {
+// N accumulator columns (tokens t0 ..) of this lane's channel.
+template <typename T, int N>
+__device__ __forceinline__ void it_store_h(const I8Params& P, const uint32_t (&v)[N], const float* sx, int t0, int n,
+                                           float sw, float bias, bool has_bias) {
   const int lane = threadIdx.x & 31;
   T* Y = static_cast<T*>(P.Y);
 #pragma unroll
-  for (int c = 0; c < 16; c += 2) {
+  for (int c = 0; c < N; c += 2) {
     const uint32_t a = Elem<T>::bits(i8_value(int(v[c]), sx[c], sw, bias, has_bias));
     const uint32_t b = Elem<T>::bits(i8_value(int(v[c + 1]), sx[c + 1], sw, bias, has_bias));
     if (P.pair) {
@@ -366,6 +367,23 @@ __device__ __forceinline__ void it_store16h(const I8Params& P, const uint32_t (&
   }
 }
 
+template <int N>
+__device__ __forceinline__ void it_store(const I8Params& P, const uint32_t (&v)[N], const float* sx, int t0, int n, float sw,
+                                         float bias, bool has_bias) {
+  if (P.out == BQG_F32) {
+    if (n < P.n) {
+      float* y = static_cast<float*>(P.Y) + (long long)t0 * P.ldy + n;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (t0 + j < P.tokens) y[j * P.ldy] = i8_value(int(v[j]), sx[j], sw, bias, has_bias);
+    }
+  } else if (P.out == BQG_F16) {
+    it_store_h<__half, N>(P, v, sx, t0, n, sw, bias, has_bias);
+  } else {
+    it_store_h<__nv_bfloat16, N>(P, v, sx, t0, n, sw, bias, has_bias);
+  }
+}
+
 // The tile's columns of one warp's 32 channels: scale, convert, store.
 __device__ __forceinline__ void it_store_tile(const I8Params& P, uint32_t lane_base, int columns, const float* sx, int t0,
                                               int n, float sw, float bias, bool has_bias) {
@@ -374,22 +392,14 @@ __device__ __forceinline__ void it_store_tile(const I8Params& P, uint32_t lane_b
   for (int c = 0; c < ncol; c += 16) {
     uint32_t v[16];
     tmem_ld16(lane_base + uint32_t(c), v);
-    if (P.out == BQG_F32) {
-      if (n < P.n) {
-        float* y = static_cast<float*>(P.Y) + (long long)(t0 + c) * P.ldy + n;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (t0 + c + j < P.tokens) y[j * P.ldy] = i8_value(int(v[j]), sx[c + j], sw, bias, has_bias);
-      }
-    } else if (P.out == BQG_F16) {
-      it_store16h<__half>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
-    } else {
-      it_store16h<__nv_bfloat16>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
-    }
+    it_store<16>(P, v, sx + c, t0 + c, n, sw, bias, has_bias);
   }
 }
 
-template <int BN>
+// SPLIT: where the tiles would leave SMs idle, a cluster of CTAs takes one tile, each a part of k; they
+// exchange their int32 sums through shared memory, each adding and storing its share of the tokens.
+// 24 x 4096 x 4096: 11.0 us on 32 SMs, 7.2 us on 128; 30 x 8192 x 1000: 19.4 and 7.6 us.
+template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kItThreads, 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
               const __grid_constant__ I8Params P) {
@@ -408,6 +418,8 @@ __global__ void __launch_bounds__(kItThreads, 1)
   uint64_t* done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   static_assert((2 * kStages + 5) * 8 + 4 <= 256, "barrier area");
+  constexpr int kSumPitch = BN + 4;  // words of a channel's sums; 16-byte accesses of a warp in different banks
+  static_assert(!SPLIT || 128 * kSumPitch * 4 <= kStages * (kABytes + kBBytes), "sums of a split tile");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -437,6 +449,9 @@ __global__ void __launch_bounds__(kItThreads, 1)
   const int ntn = (P.n + kItM - 1) / kItM, ntt = (P.tokens + BN - 1) / BN;
   const long long tiles = (long long)ntn * ntt;
   const int nk = (P.k + kItK - 1) / kItK;
+  const int split = SPLIT ? P.split : 1, rank = SPLIT ? int(cluster_ctarank()) : 0;
+  const int k0 = nk * rank / split, k1 = nk * (rank + 1) / split;
+  const long long tile0 = SPLIT ? blockIdx.x / split : blockIdx.x, tile_step = SPLIT ? tiles : gridDim.x;
   // tile i: groups of kItRaster token tiles, token tile fastest inside a group
   auto place = [&](long long i, int& tn, int& tt) {
     const long long per = (long long)kItRaster * ntn;
@@ -451,10 +466,10 @@ __global__ void __launch_bounds__(kItThreads, 1)
     if (lane == 0) {
       long long s = 0;  // stages issued
       bool ok = true;
-      for (long long i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+      for (long long i = tile0; i < tiles && ok; i += tile_step) {
         int tn, tt;
         place(i, tn, tt);
-        for (int kk = 0; kk < nk; ++kk, ++s) {
+        for (int kk = k0; kk < k1; ++kk, ++s) {
           const int st = int(s % kStages);
           if (s >= kStages && !mbar_wait(&empty[st], uint32_t(s / kStages - 1) & 1u)) {
             ok = false;
@@ -475,12 +490,12 @@ __global__ void __launch_bounds__(kItThreads, 1)
       long long s = 0;
       int it = 0;
       bool ok = true;
-      for (long long i = blockIdx.x; i < tiles && ok; i += gridDim.x, ++it) {
+      for (long long i = tile0; i < tiles && ok; i += tile_step, ++it) {
         const int buf = it & 1;
         if (it >= 2 && !mbar_wait(&acc_empty[buf], uint32_t(it / 2 - 1) & 1u)) break;
         tc_fence_after();
         const uint32_t acc = tmem + uint32_t(buf * BN);
-        for (int kk = 0; kk < nk; ++kk, ++s) {
+        for (int kk = k0; kk < k1; ++kk, ++s) {
           const int st = int(s % kStages);
           if (!mbar_wait(&full[st], uint32_t(s / kStages) & 1u)) {
             ok = false;
@@ -490,7 +505,7 @@ __global__ void __launch_bounds__(kItThreads, 1)
           const uint32_t a = smem_u32(a_ring + size_t(st) * kABytes), b = smem_u32(b_ring + size_t(st) * kBBytes);
 #pragma unroll
           for (int j = 0; j < kItK / 32; ++j)
-            umma_i8(acc, umma_desc_sw128(a + 32 * j), umma_desc_sw128(b + 32 * j), idesc, (kk > 0 || j > 0) ? 1u : 0u);
+            umma_i8(acc, umma_desc_sw128(a + 32 * j), umma_desc_sw128(b + 32 * j), idesc, (kk > k0 || j > 0) ? 1u : 0u);
           umma_commit(&empty[st]);
         }
         if (ok) umma_commit(&acc_full[buf]);
@@ -503,7 +518,7 @@ __global__ void __launch_bounds__(kItThreads, 1)
     const int et = int(threadIdx.x) - 64;  // 0..127
     const bool has_bias = P.bias != nullptr;
     int it = 0;
-    for (long long i = blockIdx.x; i < tiles; i += gridDim.x, ++it) {
+    for (long long i = tile0; i < tiles; i += tile_step, ++it) {
       const int buf = it & 1;
       int tn, tt;
       place(i, tn, tt);
@@ -516,10 +531,49 @@ __global__ void __launch_bounds__(kItThreads, 1)
       if (!mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u)) break;
       tc_fence_after();
       const uint32_t lane_base = tmem + uint32_t(buf * BN) + (uint32_t(quarter * 32) << 16);
-      it_store_tile(P, lane_base, BN, sx, t0, n, sw, bias, has_bias);
+      if constexpr (SPLIT) {  // every MMA has read its stages: their memory takes the sums
+        const uint32_t at = smem_u32(a_ring) + 4 * (quarter * 32 + lane) * kSumPitch;
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(lane_base + uint32_t(c), v);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) sts128(at + 4 * (c + j), v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+      } else {
+        it_store_tile(P, lane_base, BN, sx, t0, n, sw, bias, has_bias);
+      }
       tc_fence_before();
       mbar_arrive(&acc_empty[buf]);
     }
+  }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2) {
+      int tn, tt;
+      place(tile0, tn, tt);
+      const int quarter = warp & 3, n = tn * kItM + quarter * 32 + lane, t0 = tt * BN;
+      const bool has_bias = P.bias != nullptr;
+      const float sw = n < P.n ? __ldg(P.sw + n) : 0.f, bias = has_bias && n < P.n ? __ldg(P.bias + n) : 0.f;
+      const int share = BN / split;  // at least 4 columns
+      const uint32_t at = smem_u32(a_ring) + 4 * (quarter * 32 + lane) * kSumPitch;
+#pragma unroll 2
+      for (int c = share * rank; c < share * (rank + 1); c += 4) {
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 4
+        for (int r = 0; r < split; ++r) {
+          const float4 p = ld_dsmem_f32x4(at + 4 * c, uint32_t(r));
+          v[0] += __float_as_uint(p.x);
+          v[1] += __float_as_uint(p.y);
+          v[2] += __float_as_uint(p.z);
+          v[3] += __float_as_uint(p.w);
+        }
+        it_store<4>(P, v, sx_s + c, t0 + c, n, sw, bias, has_bias);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // a CTA's sums stay until all have read them
   }
   __syncwarp();
   tc_fence_before();
@@ -753,7 +807,7 @@ inline bool i8_encode(CUtensorMap* m, const int8_t* p, size_t pitch, int rows, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline SmemAttrOnce g_i8_attr[6];
+inline SmemAttrOnce g_i8_attr[11];
 
 template <int BN>
 inline int launch_i8_gemm(const I8Params& P, int dev, const DeviceInfo* info, cudaStream_t s) {
@@ -761,11 +815,36 @@ inline int launch_i8_gemm(const I8Params& P, int dev, const DeviceInfo* info, cu
   if (!i8_encode(&tw, P.W, size_t(P.ldw), P.n, P.k, kItM) || !i8_encode(&tx, P.X, size_t(P.ldx), P.tokens, P.k, BN))
     return BQG_ERR_CUDA;
   constexpr int slot = BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : BN == 128 ? 3 : 4;
-  const int st = g_i8_attr[slot].ensure(dev, k_i8_gemm<BN>, it_smem_bytes(BN));
-  if (st != BQG_OK) return st;
   const long long tiles = (long long)((P.n + kItM - 1) / kItM) * ((P.tokens + BN - 1) / BN);
+  if constexpr (BN <= 128) {
+    if (P.split > 1) {
+      const int st = g_i8_attr[6 + slot].ensure(dev, k_i8_gemm<BN, true>, it_smem_bytes(BN));
+      if (st != BQG_OK) return st;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(unsigned(tiles * P.split));
+      cfg.blockDim = dim3(kItThreads);
+      cfg.dynamicSmemBytes = it_smem_bytes(BN);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[2];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = unsigned(P.split);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[1].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 2;
+      if (cudaLaunchKernelEx(&cfg, k_i8_gemm<BN, true>, tw, tx, P) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return BQG_ERR_CUDA;
+      }
+      return launch_status();
+    }
+  }
+  const int st = g_i8_attr[slot].ensure(dev, k_i8_gemm<BN, false>, it_smem_bytes(BN));
+  if (st != BQG_OK) return st;
   const int grid = int(tiles < info->sm_count ? tiles : info->sm_count);
-  return launch_pdl(k_i8_gemm<BN>, dim3(unsigned(grid)), dim3(kItThreads), it_smem_bytes(BN), s, tw, tx, P);
+  return launch_pdl(k_i8_gemm<BN, false>, dim3(unsigned(grid)), dim3(kItThreads), it_smem_bytes(BN), s, tw, tx, P);
 }
 
 inline int launch_i8_gemm_pair(const I8Params& P, int dev, const DeviceInfo* info, cudaStream_t s) {
@@ -779,28 +858,41 @@ inline int launch_i8_gemm_pair(const I8Params& P, int dev, const DeviceInfo* inf
   return launch_pdl(k_i8_gemm_pair, dim3(unsigned(2 * pairs)), dim3(kI2Threads), kI2SmemBytes, s, tw, tx, P);
 }
 
-constexpr int kI8Pair = 512;  // i8_tile_tokens: tiles of CTA pairs
-// Tokens per tile: the one whose waves of tiles take the least time, a tile's 128-k stage costing
-// the larger of its MMAs (2 BN cycles) and its bytes ((128 + BN) * 128 at ~64 bytes a cycle; a pair's
-// tile 512 cycles of either).
-inline int i8_tile_tokens(int tokens, int n, int sms) {
+// How the tiles are cut: tokens per tile (kI8Pair: tiles of CTA pairs) and parts of k.  The one whose
+// waves of tiles take the fewest cycles, a tile's 128-k stage costing the larger of its MMAs (2 BN
+// cycles) and its bytes ((128 + BN) * 128 at ~64 bytes a cycle; a pair's tile 512 cycles of either); a
+// split tile's exchange of sums costs about kI8SplitCycles.
+constexpr int kI8Pair = 512;
+constexpr long long kI8SplitCycles = 3000;
+constexpr int kI8MaxSplit = 4;  // clusters of 8 do not all find room at once: 100 x 2051 x 1000 6.5 us with 4, 15.1 with 8
+struct I8Cut {
+  int tokens, split;
+};
+inline I8Cut i8_cut(int tokens, int n, int k, int sms) {
   const int ntn = (n + kItM - 1) / kItM;
-  int best = 16;
+  const long long nk = (k + kItK - 1) / kItK;
+  I8Cut best{16, 1};
   long long best_cost = -1;
   for (int bn = 16; bn <= 256; bn *= 2) {
     const long long tiles = (long long)ntn * ((tokens + bn - 1) / bn);
-    const long long waves = (tiles + sms - 1) / sms;
-    const long long stage = 2 * bn > 2 * (kItM + bn) ? 2 * bn : 2 * (kItM + bn);
-    const long long cost = waves * stage;
+    const long long stage = 2 * (kItM + bn);
+    const long long cost = (tiles + sms - 1) / sms * stage * nk;
     if (best_cost < 0 || cost <= best_cost) {
-      best = bn;
+      best = I8Cut{bn, 1};
       best_cost = cost;
+    }
+    for (int split = 2; split <= kI8MaxSplit && bn <= 128; split *= 2) {
+      const long long part = (nk + split - 1) / split * stage + kI8SplitCycles;
+      if (tiles * split <= sms && split <= nk && part < best_cost) {
+        best = I8Cut{bn, split};
+        best_cost = part;
+      }
     }
     if (bn >= tokens) break;
   }
   const long long tiles = (long long)((n + kI2M - 1) / kI2M) * ((tokens + kI2N - 1) / kI2N);
   const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
-  return waves * 512 < best_cost ? kI8Pair : best;
+  return waves * 512 * nk < best_cost ? I8Cut{kI8Pair, 1} : best;
 }
 
 }  // namespace bqg
@@ -866,7 +958,9 @@ extern "C" int qgemm_i8(const int8_t* Xq, size_t ldx, const float* sx, const int
     if (tokens <= 4) return launch_pdl(k_i8_gemv<4>, grid, dim3(kIgThreads), 0, s, P);
     return launch_pdl(k_i8_gemv<8>, grid, dim3(kIgThreads), 0, s, P);
   }
-  switch (i8_tile_tokens(tokens, n, info->sm_count)) {
+  const I8Cut cut = i8_cut(tokens, n, k, info->sm_count);
+  P.split = cut.split;
+  switch (cut.tokens) {
     case 16: return launch_i8_gemm<16>(P, dev, info, s);
     case 32: return launch_i8_gemm<32>(P, dev, info, s);
     case 64: return launch_i8_gemm<64>(P, dev, info, s);
