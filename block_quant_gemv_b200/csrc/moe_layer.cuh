@@ -434,8 +434,8 @@ __device__ __forceinline__ int ml_dealt(int n) {
 }
 
 // ---------------------------------------------------------------- selection of the experts
-// One warp, one token: the k largest of a row of BQG_MAX_EXPERTS logits, the first E of them set (ties to the lower index; NaN below everything), and
-// weights e^(l - max) over the selected ones' sum, which is the renormalised softmax.
+// One warp, one token: the k largest of a row of BQG_MAX_EXPERTS logits, the first E of them set (ties
+// to the lower index; NaN below everything), and weights e^(l - max) over the selected ones' sum, which is the renormalised softmax.
 __device__ __forceinline__ void ml_topk(const float* logits, int E, int k, int* sel_e, float* sel_w) {
   const int lane = threadIdx.x & 31;
   uint32_t key[8];  // of experts 8 lane ..; increasing with the logit; 0: none or taken, 1: NaN
@@ -1102,14 +1102,13 @@ inline MlFam ml_fam(int fmt, int hidden, int inter, const void* gate, const void
   return F;
 }
 
-// Parts of an item's k range: several steps each,
-// so that a warp's fixed cost per part stays small, but enough of them for all warps when the CTA has
-// few items.
-inline int ml_parts(int fmt, int cols, int tiles, int items_cta, int most) {
+// Parts of an item's k range: several steps (times the passes over its tokens) each, so that a warp's
+// fixed cost per part stays small, but enough of them for all warps when the CTA has few items.
+inline int ml_parts(int fmt, int cols, int tiles, int items_cta, int passes, int most) {
   const int steps = ml_steps(fmt, cols);
   int best = 1;
   for (int n = 2; n <= most && n <= steps; ++n)
-    if (n * tiles <= kMlWarps && (steps / n >= (ml_rowwise(fmt) ? 8 : 6) || items_cta * best * tiles < kMlWarps)) best = n;
+    if (n * tiles <= kMlWarps && (steps * passes / n >= (ml_rowwise(fmt) ? 8 : 6) || items_cta * best * tiles < kMlWarps)) best = n;
   return best;
 }
 
@@ -1145,9 +1144,11 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   MlParams P{};
   P.rows_cta = (L->hidden + kMlGrid - 1) / kMlGrid;
   P.parts_max = tokens <= 2 ? 12 : tokens <= 4 ? 8 : 4;  // the sums of a part take 64 bytes a token
-  const int parts2_max = tokens <= 2 ? 8 : tokens <= 4 ? 4 : 2;
+  // of phase 2: routed experts (rows of all pairs) and the shared one, whose item all warps share, since
+  // the ring frees its items in order (5 tokens of the 128-expert layer with 2 parts: 96 us)
+  const int parts2_max[2] = {tokens <= 2 ? 8 : tokens <= 4 ? 4 : 2, 8};
   const size_t sum_bytes = size_t(kMlSlots) * P.parts_max * tokens * 64;
-  const size_t y_bytes = (size_t(pairs + (sh ? tokens : 0)) * parts2_max * P.rows_cta * 4 + 127) / 128 * 128;
+  const size_t y_bytes = (size_t(pairs * parts2_max[0] + (sh ? tokens * parts2_max[1] : 0)) * P.rows_cta * 4 + 127) / 128 * 128;
   P.ring_bytes = int((kMlSmem - lay.rec_bytes - sum_bytes - y_bytes) / 128 * 128);
   P.rec_off = P.ring_bytes;
   P.sum_off = P.rec_off + int(lay.rec_bytes);
@@ -1162,9 +1163,11 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   auto up = [](int a, int b) { return (a + b - 1) / b; };
   const int items1 = up((sh ? P.fam[1].items : 0) + touched * P.fam[0].items, kMlGrid);
   const int items2 = (sh ? up(P.rows_cta, P.fam[1].nr) : 0) + touched * up(P.rows_cta, P.fam[0].nr);
-  for (MlFam& F : P.fam) {
-    F.parts1 = ml_parts(F.fmt, L->hidden, 1, items1, P.parts_max);
-    F.parts2 = ml_parts(F.fmt, F.inter, F.tiles, items2, parts2_max);
+  for (int f = 0; f < 2; ++f) {
+    MlFam& F = P.fam[f];
+    const int passes = f ? (tokens + 1) / 2 : 1;
+    F.parts1 = ml_parts(F.fmt, L->hidden, 1, items1, passes, P.parts_max);
+    F.parts2 = ml_parts(F.fmt, F.inter, F.tiles, items2, passes, parts2_max[f]);
     F.y_step = F.parts2 * P.rows_cta;
   }
   P.fam[1].y_first = pairs * P.fam[0].y_step;
