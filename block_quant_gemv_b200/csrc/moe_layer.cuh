@@ -38,11 +38,11 @@
 // added in order afterwards, so results do not depend on timing.
 //
 // Measured (us a call; weights' bytes at the HBM copy rate in brackets): 128 Q4_0 experts of 704 x 2816,
-// top 8, a shared Q8_0 expert of 2112: one token 34 [7], 5 tokens 96 [21]; 256 int4 experts of 2048 x
-// 6144, top 8: one token 44 [24], 8 tokens 265 [166].  One token: 18 us of the 44 (13 of a layer of 16
+// top 8, a shared Q8_0 expert of 2112: one token 34 [7], 5 tokens 92 [21]; 256 int4 experts of 2048 x
+// 6144, top 8: one token 44 [24], 8 tokens 235 [166].  One token: 18 us of the 44 (13 of a layer of 16
 // experts of 256 x 512, 15.5) remain with no items at all: launch, router, two grid barriers, h's way
-// through L2; with almost no MMAs it takes 42.  8 tokens: 198 with almost no MMAs, the rest is the
-// digits' way from L2 and the consumers.
+// through L2; with almost no MMAs it takes 42.  8 tokens: the digits' way
+// from L2 and the consumers.
 // dp4a, one per digit, in place of the MMA: 77 us and 410 us (256 experts, 1 and 8 tokens).
 #pragma once
 
@@ -1143,7 +1143,9 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
 
   MlParams P{};
   P.rows_cta = (L->hidden + kMlGrid - 1) / kMlGrid;
-  P.parts_max = tokens <= 2 ? 12 : tokens <= 4 ? 8 : 4;  // the sums of a part take 64 bytes a token
+  // The sums of a part take 64 bytes a token.  x's digits in global memory: more parts an item, so that
+  // fewer items' tokens share L1 (256-expert layer, 8 tokens: 265 us with 4 parts, 235 us with 6).
+  P.parts_max = tokens <= 2 ? 12 : tokens <= 4 ? 8 : lay.x_smem ? 4 : 6;
   // of phase 2: routed experts (rows of all pairs) and the shared one, whose item all warps share, since
   // the ring frees its items in order (5 tokens of the 128-expert layer with 2 parts: 96 us)
   const int parts2_max[2] = {tokens <= 2 ? 8 : tokens <= 4 ? 4 : 2, 8};
