@@ -21,7 +21,8 @@ namespace bqg {
 // ---------------------------------------------------------------- element types
 template <typename T>
 struct Elem;
-// Raw: eight values as they are stored.
+// Raw: eight values as they are stored.  most(): a running max|x| (NaN if there is one), two at a time for
+// the 16-bit types, which starts at 0 and as_float() ends.
 template <>
 struct Elem<float> {
   struct Raw {
@@ -36,6 +37,13 @@ struct Elem<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
   }
+  static __device__ __forceinline__ void most(uint32_t& top, const Raw& r) {
+    float t = __uint_as_float(top);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(t) : "f"(fabsf(__uint_as_float(r.w[i]))));
+    top = __float_as_uint(t);
+  }
+  static __device__ __forceinline__ float as_float(uint32_t top) { return __uint_as_float(top); }
 };
 struct Raw16 {
   uint32_t w[4];
@@ -61,6 +69,14 @@ struct Elem<__half> {
       v[2 * i + 1] = f.y;
     }
   }
+  static __device__ __forceinline__ void most(uint32_t& top, const Raw& r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(top) : "r"(r.w[i] & 0x7FFF7FFFu));
+  }
+  static __device__ __forceinline__ float as_float(uint32_t top) {
+    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(top) : "r"(top >> 16 | top << 16));
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(top & 0xFFFFu)));
+  }
   static __device__ __forceinline__ uint32_t bits(float f) { return __half_as_ushort(__float2half_rn(f)); }
 };
 template <>
@@ -75,6 +91,14 @@ struct Elem<__nv_bfloat16> {
       v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
     }
   }
+  static __device__ __forceinline__ void most(uint32_t& top, const Raw& r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(r.w[i] & 0x7FFF7FFFu));
+  }
+  static __device__ __forceinline__ float as_float(uint32_t top) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(top >> 16 | top << 16));
+    return __uint_as_float(top << 16);
+  }
   static __device__ __forceinline__ uint32_t bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 };
 
@@ -83,7 +107,7 @@ struct Elem<__nv_bfloat16> {
 // to kQrChunks chunks of 8 values in registers, so rows of up to TPR * 32 values are read once; longer
 // rows read the rest a second time (from L2).  Bytes bound it: 1 read and 1 write of the row; of the
 // TPR that hold a row, the smallest has the most bytes in flight (8192 x 4096 bf16: 128 threads a row
-// 22.7 us; 256, and every rounding decided the long way, 40 us), the largest the shortest way for few
+// 22.2 us; 256, and every rounding decided the long way, 40 us), the largest the shortest way for few
 // rows.  fp32 rows of 4096: 27.1 us, 6.2 TB/s.
 //
 // The rounding is decided exactly.  t = x * (1 / s) + 1.5 * 2^23 is rounded once, to a whole number
@@ -129,13 +153,7 @@ __global__ void __launch_bounds__(TPR == 32 ? kQrThreads : TPR) k_quantize_rows(
       if (i0 + j < k) Elem<T>::set(r, j, x[i0 + j]);
     return r;
   };
-  float top = 0.f;  // max|x|, NaN if there is one
-  auto take = [&](const Raw& r) {
-    float v[8];
-    Elem<T>::values(r, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(v[j])));
-  };
+  uint32_t top = 0u;
   Raw keep[kQrChunks];
 #pragma unroll
   for (int c = 0; c < kQrChunks; ++c) {
@@ -144,10 +162,10 @@ __global__ void __launch_bounds__(TPR == 32 ? kQrThreads : TPR) k_quantize_rows(
     if (i0 < kmain) keep[c] = load(i0);
   }
 #pragma unroll
-  for (int c = 0; c < kQrChunks; ++c) take(keep[c]);
-  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) take(load(i0));
+  for (int c = 0; c < kQrChunks; ++c) Elem<T>::most(top, keep[c]);
+  for (int i0 = (kQrChunks * TPR + tid) * 8; i0 < k; i0 += TPR * 8) Elem<T>::most(top, load(i0));
   // as an unsigned integer, which keeps the order and puts Inf and NaN above every finite value
-  uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(Elem<T>::as_float(top)));
   if (TPR > 32) {
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = most;
     __syncthreads();
