@@ -63,3 +63,14 @@ def test_in_a_graph_and_on_two_streams():
     xq, sx = bqg.quantize_rows_i8(q.float())
     assert torch.equal(y, bqg.qgemm_i8(xq, sx, w, one, torch.float32))
     assert bqg.bqg_device_errors() == 0
+
+
+@pytest.mark.parametrize("tokens,k,n", [(25000, 64, 100), (20003, 200, 128)])
+def test_many_tokens_few_channels(tokens, k, n):
+    """128 x 256 tiles of single CTAs: one row of channels, more tiles than CTA pairs."""
+    need_gpu()
+    q, w = int8_rows(1, tokens, k), int8_rows(2, n, k)
+    one = torch.ones(tokens, device="cuda")
+    y = bqg.qgemm_i8(q, one, w, one[:n], torch.float32)
+    assert torch.equal(y.double(), q.double() @ w.double().T)
+    assert bqg.bqg_device_errors() == 0
