@@ -375,7 +375,8 @@ struct MlShared {
   int4 desc[kMlSlots][3];
   int seq[kMlSlots];     // the item in the slot
   int start[kMlSlots];   // its place in the ring
-  int abort;
+  int abort;             // a bounded wait gave up (any warp, at any time)
+  int h_done;            // barrier 2 was passed: thread 0's word, the same for every consumer warp
   int n_active, n1;      // touched experts, the CTA's items of phase 1
   float red[kMlWarps][kMlMaxTokens];
   uint32_t xmax[kMlMaxTokens];
@@ -419,6 +420,13 @@ __device__ __forceinline__ bool ml_wait_seq(int* seq, int i) {
     }
     __nanosleep(40);
   }
+}
+// A warp goes on or gives up as a whole: MMAs and shuffles need all of its lanes.
+__device__ __forceinline__ bool ml_all(bool v) { return __all_sync(0xffffffffu, v); }
+// Warps may see the word change at different times: it may steer a warp's own work, but no barrier of several
+// warps lies behind a branch on it.
+__device__ __forceinline__ bool ml_aborted(const MlShared& S) {
+  return __any_sync(0xffffffffu, *(const volatile int*)&S.abort != 0);
 }
 // All warps: the lists are made.  A hardware barrier, since warps that poll slow down the one that selects.
 // The warp that made them only arrives: it has items of the shared expert to finish before the others come.
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       if (pass == 1) {
         ml_list_sync();
         listed = true;
-        ok = !*(volatile int*)&S.abort;
+        ok = !ml_aborted(S);
         if (!ok) break;
         n1 = S.n1;
       }
@@ -615,7 +623,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
               if (!wrapped && head + need > P.ring_bytes && need <= oldest) head = 0;
               if (head + need <= (i > tail && head <= oldest ? oldest : P.ring_bytes)) break;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&S.done[tail % kMlSlots], uint32_t(tail / kMlSlots) & 1u));
+            ok = ml_all(mbar_wait(&S.done[tail % kMlSlots], uint32_t(tail / kMlSlots) & 1u));
             if (!ok) break;
             ++tail;
             if (tail < i) oldest = S.start[tail % kMlSlots];
@@ -623,7 +631,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
           // the slot's sums, where the helpers read them
           const int before = i - kMlSlots;
           if (ok && before >= 0 && before < n1)
-            ok = __all_sync(0xffffffffu, mbar_wait(&S.empty[slot], uint32_t(before / kMlSlots) & 1u));
+            ok = ml_all(mbar_wait(&S.empty[slot], uint32_t(before / kMlSlots) & 1u));
           if (!ok) break;
           if (lane == l) {
             fence_proxy_async_smem();
@@ -680,7 +688,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
           }
         }
       } else {
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.topk_ready, 0)) && !*(volatile int*)&S.abort;
+        ok = ml_all(mbar_wait(&S.topk_ready, 0)) && !ml_aborted(S);
         __syncwarp();
         if (ok) ml_list(S, P.tokens, P.top_k);
       }
@@ -704,7 +712,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       if (!listed) ml_list_sync();
       listed = true;
       end = S.n1;
-      ok = ok && !*(volatile int*)&S.abort;
+      ok = ok && !ml_aborted(S);
     };
     if (warp == kMlWarps + 1) {
       ml_list_arrive();
@@ -715,8 +723,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       if (i >= ns && !listed) need_list();
       if (!ok || i >= end) break;
       const int slot = i % kMlSlots;
-      ok = __all_sync(0xffffffffu, ml_wait_seq(&S.seq[slot], i)) &&
-           __all_sync(0xffffffffu, mbar_wait(&S.done[slot], uint32_t(i / kMlSlots) & 1u));
+      ok = ml_all(ml_wait_seq(&S.seq[slot], i)) && ml_all(mbar_wait(&S.done[slot], uint32_t(i / kMlSlots) & 1u));
       if (!ok) break;
       const int fam = i < ns ? 1 : 0;
       const MlFam& F = P.fam[fam];
@@ -845,7 +852,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     auto need_list = [&]() {
       if (!listed) {
         ml_list_sync();
-        ok = ok && !*(volatile int*)&S.abort;
+        ok = ok && !ml_aborted(S);
         listed = true;
       }
       return ok;
@@ -853,7 +860,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
     if (!P.x_smem) {  // the rows in global memory are complete behind barrier 1
       if (tid == 0 && !ml_wait(P.bar, uint32_t(G))) *(volatile int*)&S.abort = 1;
       ml_consumers_sync();
-      ok = !*(volatile int*)&S.abort;
+      ok = !ml_aborted(S);
     }
 
     const uint32_t ring_s = smem_u32(smem);
@@ -889,10 +896,8 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       const int count = groups + (unit == 0 ? kMlWarps - size * groups : 0);
       for (int i = grp < groups ? i0 + grp : done_items; i < done_items && ok; i += groups) {
         const int slot = i % kMlSlots;
-        if (!ml_wait_seq(&S.seq[slot], i)) {
-          ok = false;
-          break;
-        }
+        // one vote for both waits; a lane that gave up on the first follows no address of the descriptor
+        const bool placed = ml_wait_seq(&S.seq[slot], i);
         const int4 d = ld_desc(&S.desc[slot][0]), o = ld_desc(&S.desc[slot][1]);
         const int np = d.w;
         // The lane's two rows, row tile + g of either block.  Odd g take them the other way round: with
@@ -900,14 +905,14 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         // different banks.
         const int t0 = min(tile + g, o.z - 1), t1 = min(tile + g, (o.w > 0 ? o.w : o.z) - 1);
         float rs0 = 1.f, rs1 = 1.f;
-        if (ml_rowwise(fmt)) {
+        if (ml_rowwise(fmt) && placed) {
           const int4 at = ld_desc(&S.desc[slot][2]);
           rs0 = __ldg(reinterpret_cast<const float*>(uint64_t(uint32_t(at.x)) | uint64_t(uint32_t(at.y)) << 32) + t0);
           if (o.w > 0) rs1 = __ldg(reinterpret_cast<const float*>(uint64_t(uint32_t(at.z)) | uint64_t(uint32_t(at.w)) << 32) + t1);
         }
         const uint32_t b0 = ring_s + uint32_t(o.x + t0 * rb), b1 = ring_s + uint32_t(o.y + t1 * rb);
         const uint32_t a0 = g & 1 ? b1 : b0, a1 = g & 1 ? b0 : b1;
-        if (!mbar_wait(&S.full[slot], uint32_t(i / kMlSlots) & 1u)) {
+        if (!ml_all(placed && mbar_wait(&S.full[slot], uint32_t(i / kMlSlots) & 1u))) {
           ok = false;
           break;
         }
@@ -955,9 +960,10 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         if (!mbar_wait(&S.h_ready, 0)) *(volatile int*)&S.abort = 1;
         ml_arrive(P.bar + kMlBar);
         if (*(volatile int*)&S.abort || !ml_wait(P.bar + kMlBar, uint32_t(G))) *(volatile int*)&S.abort = 1;
+        S.h_done = !*(volatile int*)&S.abort;
       }
       ml_consumers_sync();
-      if (!*(volatile int*)&S.abort) {
+      if (S.h_done) {
         // once per CTA: a single line that 148 SMs ask for gives less than one answer a clock
         if (tid < pairs + P.tokens) S.hmax[tid] = __ldcg(P.bar + kMlHmax + tid);
         ml_consumers_sync();
@@ -974,12 +980,12 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         }
         ml_consumers_sync();
       }
-      ok = ok && !*(volatile int*)&S.abort;
+      ok = ok && !ml_aborted(S);
     }
     if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
     ml_consumers_sync();
     // y: the parts of a pair's row added in order, then the pairs in slot order
-    if (!*(volatile int*)&S.abort) {
+    if (!ml_aborted(S)) {
       const int all = pairs + (P.has_shared ? P.tokens : 0);
       for (int i = tid; i < all * rows; i += kMlConsumers) {
         const int p = i / rows, r = i - p * rows, fam = p >= pairs ? 1 : 0;
@@ -992,7 +998,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       }
     }
     ml_consumers_sync();
-    if (!*(volatile int*)&S.abort)
+    if (!ml_aborted(S))
       for (int i = tid; i < P.tokens * rows; i += kMlConsumers) {
         const int t = i / rows, r = i - t * rows;
         float acc = 0.f;

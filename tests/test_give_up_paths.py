@@ -1,0 +1,72 @@
+"""What kernels do after a bounded wait gave up, read from their source: a warp takes one decision for all
+of its lanes (its MMAs, shuffles and tensor-memory loads need them), and no barrier that several warps
+count on lies behind a decision that they take separately.  A kernel that breaks either rule may never
+end, so this is not tried out on a GPU."""
+import os
+import re
+
+import pytest
+
+from tests.conftest import ROOT
+
+CSRC = os.path.join(ROOT, "block_quant_gemv_b200", "csrc")
+BARRIERS = ("ml_consumers_sync(", "ml_list_sync(", "bar.sync", "__syncthreads(", "cluster_sync(")
+
+
+def source(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def closing(text, at, pair):
+    """The place behind the bracket that closes the one at `at`."""
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {pair[0]: 1, pair[1]: -1}.get(text[i], 0)
+        if depth == 0:
+            return i + 1
+    raise AssertionError("no closing bracket")
+
+
+def branches(text):
+    """(condition, body) of every `if` and `while` and the condition of every `for`."""
+    for m in re.finditer(r"\b(?:if|while|for) (?:constexpr )?\(", text):
+        end = closing(text, m.end() - 1, "()")
+        cond = text[m.end():end - 1]
+        rest = text[end:].lstrip()
+        start = len(text) - len(rest) if rest else end
+        if text[start] == "{":
+            yield cond, text[start:closing(text, start, "{}")]
+        else:
+            yield cond, text[start:text.index(";", start)]
+
+
+def single_thread(cond):
+    return re.search(r"\b(tid|threadIdx\.x|lane) == \w+", cond) is not None
+
+
+def test_no_barrier_behind_the_abort_word():
+    for cond, body in branches(source("moe_layer.cuh")):
+        if "abort" in cond and not single_thread(cond):
+            assert not any(b in body for b in BARRIERS), cond
+
+
+def waits(text, names):
+    """Every call of a bounded wait outside the code of single threads, with the text before it."""
+    alone = [body for cond, body in branches(text) if single_thread(cond)]
+    for m in re.finditer(r"\b(?:%s)\(" % "|".join(names), text):
+        before, line = text[:m.start()], text[text.rfind("\n", 0, m.start()) + 1:text.find("\n", m.start())]
+        if "__device__" in line or single_thread(line) or any(line in body for body in alone):
+            continue
+        yield before, line
+
+
+@pytest.mark.parametrize("name,vote", [("moe_layer.cuh", "ml_all(")])
+def test_a_warp_decides_as_a_whole(name, vote):
+    seen = 0
+    for before, line in waits(source(name), ("mbar_wait", "ml_wait_seq")):
+        if before.rstrip().endswith((";", "{", ")")):  # a wait whose answer nobody uses
+            continue
+        seen += 1
+        assert before.endswith(vote), line
+    assert seen > 0
