@@ -896,8 +896,10 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       const int count = groups + (unit == 0 ? kMlWarps - size * groups : 0);
       for (int i = grp < groups ? i0 + grp : done_items; i < done_items && ok; i += groups) {
         const int slot = i % kMlSlots;
-        // one vote for both waits; a lane that gave up on the first follows no address of the descriptor
-        const bool placed = ml_wait_seq(&S.seq[slot], i);
+        if (!ml_all(ml_wait_seq(&S.seq[slot], i))) {
+          ok = false;
+          break;
+        }
         const int4 d = ld_desc(&S.desc[slot][0]), o = ld_desc(&S.desc[slot][1]);
         const int np = d.w;
         // The lane's two rows, row tile + g of either block.  Odd g take them the other way round: with
@@ -905,14 +907,14 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         // different banks.
         const int t0 = min(tile + g, o.z - 1), t1 = min(tile + g, (o.w > 0 ? o.w : o.z) - 1);
         float rs0 = 1.f, rs1 = 1.f;
-        if (ml_rowwise(fmt) && placed) {
+        if (ml_rowwise(fmt)) {
           const int4 at = ld_desc(&S.desc[slot][2]);
           rs0 = __ldg(reinterpret_cast<const float*>(uint64_t(uint32_t(at.x)) | uint64_t(uint32_t(at.y)) << 32) + t0);
           if (o.w > 0) rs1 = __ldg(reinterpret_cast<const float*>(uint64_t(uint32_t(at.z)) | uint64_t(uint32_t(at.w)) << 32) + t1);
         }
         const uint32_t b0 = ring_s + uint32_t(o.x + t0 * rb), b1 = ring_s + uint32_t(o.y + t1 * rb);
         const uint32_t a0 = g & 1 ? b1 : b0, a1 = g & 1 ? b0 : b1;
-        if (!ml_all(placed && mbar_wait(&S.full[slot], uint32_t(i / kMlSlots) & 1u))) {
+        if (!ml_all(mbar_wait(&S.full[slot], uint32_t(i / kMlSlots) & 1u))) {
           ok = false;
           break;
         }
