@@ -414,6 +414,19 @@ __device__ __forceinline__ void it_store_tile(const I8Params& P, uint32_t lane_b
   }
 }
 
+// The storing warps' barrier (THREADS of them), which tells each whether all have what they waited for: a warp
+// whose wait gave up comes here once more, and all of them leave together.
+template <int THREADS>
+__device__ __forceinline__ bool it_all_go_on(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(uint32_t(ok)), "n"(THREADS)
+      : "memory");
+  return all != 0;
+}
+
 // SPLIT: where the tiles would leave SMs idle, a cluster of CTAs takes one tile, each a part of k; they
 // exchange their int32 sums through shared memory, each adding and storing its share of the tokens.
 // 24 x 4096 x 4096: 11.0 us on 32 SMs, 7.2 us on 128; 30 x 8192 x 1000: 19.4 and 7.6 us.
@@ -536,6 +549,7 @@ __global__ void __launch_bounds__(kItThreads, 1)
     const int et = int(threadIdx.x) - 64;  // 0..127
     const bool has_bias = P.bias != nullptr;
     int it = 0;
+    bool ok = true;
     for (long long i = tile0; i < tiles; i += tile_step, ++it) {
       const int buf = it & 1;
       int tn, tt;
@@ -545,8 +559,9 @@ __global__ void __launch_bounds__(kItThreads, 1)
       for (int c = et; c < BN; c += 128) sx[c] = t0 + c < P.tokens ? __ldg(P.sx + t0 + c) : 0.f;
       const float sw = n < P.n ? __ldg(P.sw + n) : 0.f;
       const float bias = has_bias && n < P.n ? __ldg(P.bias + n) : 0.f;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      if (!mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u)) break;
+      if (!it_all_go_on<128>(ok)) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u));
+      if (!ok) continue;
       tc_fence_after();
       const uint32_t lane_base = tmem + uint32_t(buf * BN) + (uint32_t(quarter * 32) << 16);
       if constexpr (SPLIT) {  // every MMA has read its stages: their memory takes the sums
@@ -759,6 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI2Threads, 1)
     const int et = int(threadIdx.x) - 64;  // 0..255
     const bool has_bias = P.bias != nullptr;
     int it = 0;
+    bool ok = true;
     for (long long i = blockIdx.x / 2; i < tiles; i += pairs, ++it) {
       const int buf = it & 1;
       int tn, tt;
@@ -768,8 +784,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI2Threads, 1)
       sx[et] = t0 + et < P.tokens ? __ldg(P.sx + t0 + et) : 0.f;
       const float sw = n < P.n ? __ldg(P.sw + n) : 0.f;
       const float bias = has_bias && n < P.n ? __ldg(P.bias + n) : 0.f;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (!mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u)) break;
+      if (!it_all_go_on<256>(ok)) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], uint32_t(it / 2) & 1u));
+      if (!ok) continue;
       tc_fence_after();
       it_store_tile(P, tmem + uint32_t(buf * kI2N + col) + (uint32_t(quarter * 32) << 16), kI2Half, sx + col, t0 + col, n, sw,
                     bias, has_bias);

@@ -61,7 +61,7 @@ def waits(text, names):
         yield before, line
 
 
-@pytest.mark.parametrize("name,vote", [("moe_layer.cuh", "ml_all(")])
+@pytest.mark.parametrize("name,vote", [("moe_layer.cuh", "ml_all("), ("i8.cuh", "__all_sync(0xffffffffu, ")])
 def test_a_warp_decides_as_a_whole(name, vote):
     seen = 0
     for before, line in waits(source(name), ("mbar_wait", "ml_wait_seq")):
@@ -70,3 +70,18 @@ def test_a_warp_decides_as_a_whole(name, vote):
         seen += 1
         assert before.endswith(vote), line
     assert seen > 0
+
+
+def test_storing_warps_leave_their_loop_together():
+    """The int8 products' storing warps meet at a barrier in every tile: none of them leaves the loop but by
+    that barrier's own answer, which is the same for all."""
+    text = source("i8.cuh")
+    assert "bar.sync" not in text
+    alone = [body for cond, body in branches(text) if single_thread(cond)]
+    loops = [body for cond, body in branches(text) if "it_all_go_on<" in body and not any(body in a for a in alone)
+             and re.match(r"long long i = ", cond)]
+    assert len(loops) == 2
+    for loop in loops:
+        leaves = [cond for cond, body in branches(loop) if re.search(r"\b(break|return)\b", body)]
+        assert len(leaves) == len(re.findall(r"\b(?:break|return)\b", loop)) == 1
+        assert leaves[0].startswith("!it_all_go_on<")
