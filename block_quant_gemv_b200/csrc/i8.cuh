@@ -765,9 +765,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI2Threads, 1)
           }
           if (ok) umma_commit_pair(&acc_full[buf]);
         }
-        umma_commit_pair(done);  // every MMA issued here has completed before tensor memory is freed
+        umma_commit_pair(done);
       }
-      mbar_wait(done, 0);
     }
   } else {
     const int quarter = warp & 3, col = (warp - 2) / 4 * kI2Half;
@@ -796,6 +795,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI2Threads, 1)
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_cta(&acc_empty[buf])) : "memory");
     }
   }
+  // Every MMA has completed before tensor memory is freed and the barriers that its commits arrive on go.
+  // Waited for behind the storing warps, which the last tile's MMAs let go: the second CTA, which issues
+  // none, would otherwise wait from the start on, and a product of more than two seconds would look stuck.
+  __syncthreads();
+  if (threadIdx.x == 32) mbar_wait(done, 0);
   __syncwarp();
   tc_fence_before();
   cluster_sync();  // neither CTA's memory is freed while the other still uses it

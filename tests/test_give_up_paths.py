@@ -85,3 +85,14 @@ def test_storing_warps_leave_their_loop_together():
         leaves = [cond for cond, body in branches(loop) if re.search(r"\b(break|return)\b", body)]
         assert len(leaves) == len(re.findall(r"\b(?:break|return)\b", loop)) == 1
         assert leaves[0].startswith("!it_all_go_on<")
+
+
+def test_no_wait_lasts_as_long_as_the_product():
+    """The second CTA of a pair issues no MMAs: it waits for the last of them only once its storing warps are
+    through, since a bounded wait over a whole long product would give up."""
+    text = source("i8.cuh")
+    kernel = text[text.index("k_i8_gemm_pair("):]
+    kernel = kernel[:closing(kernel, kernel.index("{"), "{}")]
+    assert kernel.count("mbar_wait(done") == 1
+    wait = kernel.index("mbar_wait(done")
+    assert kernel.index("it_store_tile(") < kernel.rindex("__syncthreads()", 0, wait) < wait
