@@ -232,8 +232,9 @@ struct I8Params {
 };
 
 __device__ __forceinline__ float i8_value(int sum, float sx, float sw, float bias, bool has_bias) {
-  const float v = float(sum) * sx * sw;
-  return has_bias ? v + bias : v;
+  // spelled out, so that no copy of this fuses a product with the bias: all paths round alike
+  const float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), sx), sw);
+  return has_bias ? __fadd_rn(v, bias) : v;
 }
 
 __device__ __forceinline__ void i8_store(const I8Params& P, long long t, int n, float v) {

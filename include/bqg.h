@@ -207,7 +207,9 @@ BQG_API int qgemm_prefill(int fmt, const void* W, const void* X, void* Y, int to
  *   rows >= 1.   1 <= k <= BQG_MAX_I8_COLS.
  *
  * qgemm_i8: Y[t, n] = sx[t] * sw[n] * sum_i Xq[t, i] * Wq[n, i] (+ bias[n]).  The sums are exact in
- * int32 (any int8 values); the scalings run in fp32, Y is rounded once.  Deterministic.
+ * int32 (any int8 values); fp32((fp32(sum) * sx[t]) * sw[n]) + bias[n], each operation rounded to fp32
+ * (so sum * sx[t] beyond fp32's range is Inf, whatever sw[n]), then the store to out_type.  Every
+ * number of tokens gives the same bits.  Deterministic.
  *   Xq     device int8, row t at Xq + t * ldx.   sx  device fp32 [tokens].
  *   Wq     device int8, row n at Wq + n * ldw.   sw  device fp32 [n].   bias  device fp32 [n] or NULL.
  *          ldx, ldw >= k, multiples of 16; Xq and Wq 16-byte aligned; the bytes behind a row's k
