@@ -34,7 +34,7 @@ ACT_GELU_TANH, ACT_SILU = 1, 2
 MOE_PATH_AUTO, MOE_PATH_CUDA_CORES, MOE_PATH_TENSOR_CORES = 0, 1, 2
 MOE_TC_MIN_TOKENS = 8
 MAX_COLS, MAX_BATCH, MAX_EXPERTS, MAX_TOPK, MAX_MOE_COLS = 15360, 256, 256, 8, 7168
-MAX_I8_COLS, MOE_LAYER_MAX_TOKENS, MOE_LAYER_STATE_BYTES = 65536, 8, 1024
+MAX_I8_COLS, MAX_I8_ROWS, MOE_LAYER_MAX_TOKENS, MOE_LAYER_STATE_BYTES = 65536, 2147483136, 8, 1024
 DEVERR_TIMEOUT, DEVERR_EXPERT_ID = 0x1, 0x2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

@@ -811,6 +811,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI2Threads, 1)
 }
 
 // ---------------------------------------------------------------- host side
+// The last tile's rows and columns, past the tensors' ends too, are 32-bit indexes.
+static_assert(0x7FFFFFFF - BQG_MAX_I8_ROWS >= kI2M && 0x7FFFFFFF - BQG_MAX_I8_ROWS >= 256, "a tile past the last row");
 inline size_t i8_type_bytes(int type) { return type == BQG_F32 ? 4 : (type == BQG_F16 || type == BQG_BF16) ? 2 : 0; }
 
 template <typename T>
@@ -943,7 +945,7 @@ extern "C" int quantize_rows_i8(int type, const void* X, size_t ldx, int8_t* Xq,
   if (X == nullptr || Xq == nullptr || scale == nullptr || rows < 1 || k < 1) return BQG_ERR_ARG;
   const size_t size = i8_type_bytes(type);
   if (size == 0) return BQG_ERR_ARG;
-  if (k > BQG_MAX_I8_COLS) return BQG_ERR_LIMIT;
+  if (k > BQG_MAX_I8_COLS || rows > BQG_MAX_I8_ROWS) return BQG_ERR_LIMIT;
   if (ldx < size_t(k) || ldq < size_t(k) || ldq % 16 != 0) return BQG_ERR_SHAPE;
   if (!aligned(X, size) || !aligned(Xq, 16) || !aligned(scale, 4)) return BQG_ERR_ALIGN;
   int dev;
@@ -963,7 +965,7 @@ extern "C" int qgemm_i8(const int8_t* Xq, size_t ldx, const float* sx, const int
     return BQG_ERR_ARG;
   const size_t size = i8_type_bytes(out_type);
   if (size == 0) return BQG_ERR_ARG;
-  if (k > BQG_MAX_I8_COLS) return BQG_ERR_LIMIT;
+  if (k > BQG_MAX_I8_COLS || tokens > BQG_MAX_I8_ROWS || n > BQG_MAX_I8_ROWS) return BQG_ERR_LIMIT;
   if (ldx < size_t(k) || ldw < size_t(k) || ldy < size_t(n) || ldx % 16 != 0 || ldw % 16 != 0) return BQG_ERR_SHAPE;
   if (!aligned(Xq, 16) || !aligned(Wq, 16) || !aligned(sx, 4) || !aligned(sw, 4) || !aligned(bias, 4) ||
       !aligned(Y, size))

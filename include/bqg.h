@@ -100,6 +100,7 @@ enum bqg_moe_path { BQG_MOE_PATH_AUTO = 0, BQG_MOE_PATH_CUDA_CORES = 1, BQG_MOE_
 #define BQG_MAX_MOE_COLS 7168    /* largest hidden / inter / shared_inter of moe_forward   */
 #define BQG_MOE_LAYER_MAX_TOKENS 8 /* largest token count of moe_layer                      */
 #define BQG_MAX_I8_COLS 65536    /* largest k of quantize_rows_i8 / qgemm_i8               */
+#define BQG_MAX_I8_ROWS 2147483136 /* largest rows / tokens / n of quantize_rows_i8 / qgemm_i8 (2^31 - 512) */
 
 /* Device-side error bits, reported by bqg_device_errors(). */
 #define BQG_DEVERR_TIMEOUT 0x1   /* a bounded in-kernel wait gave up (the kernel returned early) */
@@ -204,7 +205,8 @@ BQG_API int qgemm_prefill(int fmt, const void* W, const void* X, void* Y, int to
  *   X      device [rows x k], row t at X + t * ldx elements (ldx >= k), aligned to its element.
  *   Xq     device int8, row t at Xq + t * ldq (ldq >= k, a multiple of 16), 16-byte aligned; the
  *          ldq - k bytes behind a row are left as they are.   scale  device fp32 [rows].
- *   rows >= 1.   1 <= k <= BQG_MAX_I8_COLS.
+ *          Xq must not overlap X.
+ *   1 <= rows <= BQG_MAX_I8_ROWS.   1 <= k <= BQG_MAX_I8_COLS.
  *
  * qgemm_i8: Y[t, n] = sx[t] * sw[n] * sum_i Xq[t, i] * Wq[n, i] (+ bias[n]).  The sums are exact in
  * int32 (any int8 values); fp32((fp32(sum) * sx[t]) * sw[n]) + bias[n], each operation rounded to fp32
@@ -216,7 +218,7 @@ BQG_API int qgemm_prefill(int fmt, const void* W, const void* X, void* Y, int to
  *          values are not used.
  *   Y      device, out_type (BQG_F32, BQG_F16, BQG_BF16), row t at Y + t * ldy elements (ldy >= n),
  *          aligned to its element; must not overlap the inputs.
- *   tokens, n >= 1.   1 <= k <= BQG_MAX_I8_COLS. */
+ *   1 <= tokens, n <= BQG_MAX_I8_ROWS.   1 <= k <= BQG_MAX_I8_COLS. */
 BQG_API int quantize_rows_i8(int type, const void* X, size_t ldx, int8_t* Xq, size_t ldq, float* scale, int rows, int k,
                              void* stream);
 BQG_API int qgemm_i8(const int8_t* Xq, size_t ldx, const float* sx, const int8_t* Wq, size_t ldw, const float* sw,
