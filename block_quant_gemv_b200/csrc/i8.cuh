@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "host_common.h"
+#include "i8_cut.h"
 #include "tcgen05.cuh"
 
 namespace bqg {
@@ -332,8 +333,6 @@ __global__ void __launch_bounds__(kIgThreads) k_i8_gemv(const __grid_constant__ 
 //   warps 2-5  scale, convert and store the other accumulator (one warp per 32 lanes)
 // Persistent: CTA b takes tiles b, b + grid, ...
 constexpr int kItThreads = 192;
-constexpr int kItM = 128;
-constexpr int kItK = 128;
 constexpr int kItRaster = 8;  // token tiles walked together (their X and the W tiles of a wave stay in L2)
 __host__ __device__ constexpr int it_stage_bytes(int bn) { return (kItM + bn) * kItK; }
 __host__ __device__ constexpr int it_stages(int bn) {
@@ -626,7 +625,7 @@ __global__ void __launch_bounds__(kItThreads, 1)
 // more than an SM gets from L2.  The warps' parts are k_i8_gemm's, but eight warps store.
 // 8192 tokens, k 4096, n 14336, bf16 out: 457 us as 128 x 256 tiles (2.1 POP/s), 435 us with four storing
 // warps (a tile's 256 columns took longer than its 32 stages), 308 us (3.1 POP/s; tensor pipe 82 % active).
-constexpr int kI2M = 256, kI2N = 256, kI2Half = 128;
+constexpr int kI2Half = 128;
 constexpr int kI2Threads = 320;  // 8 warps store: a quarter of the channels and half of the tokens each
 constexpr int kI2StageBytes = 2 * kI2Half * kItK;
 constexpr int kI2Stages = 6;
@@ -849,7 +848,7 @@ inline bool i8_encode(CUtensorMap* m, const int8_t* p, size_t pitch, int rows, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline SmemAttrOnce g_i8_attr[11];
+inline SmemAttrOnce g_i8_attr[10];  // tiles of 16 to 256 tokens, of pairs, and of 16 to 128 in parts of k
 
 template <int BN>
 inline int launch_i8_gemm(const I8Params& P, int dev, const DeviceInfo* info, cudaStream_t s) {
@@ -900,42 +899,40 @@ inline int launch_i8_gemm_pair(const I8Params& P, int dev, const DeviceInfo* inf
   return launch_pdl(k_i8_gemm_pair, dim3(unsigned(2 * pairs)), dim3(kI2Threads), kI2SmemBytes, s, tw, tx, P);
 }
 
-// How the tiles are cut: tokens per tile (kI8Pair: tiles of CTA pairs) and parts of k.  The one whose
-// waves of tiles take the fewest cycles, a tile's 128-k stage costing the larger of its MMAs (2 BN
-// cycles) and its bytes ((128 + BN) * 128 at ~64 bytes a cycle; a pair's tile 512 cycles of either); a
-// split tile's exchange of sums costs about kI8SplitCycles.
-constexpr int kI8Pair = 512;
-constexpr long long kI8SplitCycles = 3000;
-constexpr int kI8MaxSplit = 4;  // clusters of 8 do not all find room at once: 100 x 2051 x 1000 6.5 us with 4, 15.1 with 8
-struct I8Cut {
-  int tokens, split;
-};
-inline I8Cut i8_cut(int tokens, int n, int k, int sms) {
-  const int ntn = (n + kItM - 1) / kItM;
-  const long long nk = (k + kItK - 1) / kItK;
-  I8Cut best{16, 1};
-  long long best_cost = -1;
-  for (int bn = 16; bn <= 256; bn *= 2) {
-    const long long tiles = (long long)ntn * ((tokens + bn - 1) / bn);
-    const long long stage = 2 * (kItM + bn);
-    const long long cost = (tiles + sms - 1) / sms * stage * nk;
-    if (best_cost < 0 || cost <= best_cost) {
-      best = I8Cut{bn, 1};
-      best_cost = cost;
+// Clusters of 2 and of 4 CTAs that run at once on the device (a CTA of k_i8_gemm takes a whole SM, and a
+// cluster's CTAs one cluster of SMs: 74 of 2, 33 of 4 on a B200).  Asked once per device.
+inline I8Clusters i8_clusters(int dev) {
+  static std::atomic<int> known[kMaxDevices][2] = {};  // count + 1
+  int n[2] = {0, 0};
+  for (int i = 0; i < 2; ++i) {
+    n[i] = known[dev][i].load(std::memory_order_relaxed) - 1;
+    if (n[i] >= 0) continue;
+    n[i] = 0;
+    if (g_i8_attr[6].ensure(dev, k_i8_gemm<16, true>, it_smem_bytes(16)) != BQG_OK) continue;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2u << i);
+    cfg.blockDim = dim3(kItThreads);
+    cfg.dynamicSmemBytes = it_smem_bytes(16);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2u << i;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int count = 0;
+    if (cudaOccupancyMaxActiveClusters(&count, k_i8_gemm<16, true>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      continue;  // no parts of k in this call; the next one asks again
     }
-    for (int split = 2; split <= kI8MaxSplit && bn <= 128; split *= 2) {
-      const long long part = (nk + split - 1) / split * stage + kI8SplitCycles;
-      if (tiles * split <= sms && split <= nk && part < best_cost) {
-        best = I8Cut{bn, split};
-        best_cost = part;
-      }
-    }
-    if (bn >= tokens) break;
+    n[i] = count;
+    known[dev][i].store(count + 1, std::memory_order_relaxed);
   }
-  const long long tiles = (long long)((n + kI2M - 1) / kI2M) * ((tokens + kI2N - 1) / kI2N);
-  const long long waves = (tiles + sms / 2 - 1) / (sms / 2);
-  return waves * 512 * nk < best_cost ? I8Cut{kI8Pair, 1} : best;
+  return I8Clusters{n[0], n[1]};
 }
+static_assert(it_smem_bytes(16) > 114 * 1024 && it_smem_bytes(32) > 114 * 1024 && it_smem_bytes(64) > 114 * 1024 &&
+                  it_smem_bytes(128) > 114 * 1024,
+              "one CTA an SM, whatever the tile");
 
 }  // namespace bqg
 
@@ -1000,7 +997,7 @@ extern "C" int qgemm_i8(const int8_t* Xq, size_t ldx, const float* sx, const int
     if (tokens <= 4) return launch_pdl(k_i8_gemv<4>, grid, dim3(kIgThreads), 0, s, P);
     return launch_pdl(k_i8_gemv<8>, grid, dim3(kIgThreads), 0, s, P);
   }
-  const I8Cut cut = i8_cut(tokens, n, k, info->sm_count);
+  const I8Cut cut = i8_cut(tokens, n, k, info->sm_count, i8_clusters(dev));
   P.split = cut.split;
   switch (cut.tokens) {
     case 16: return launch_i8_gemm<16>(P, dev, info, s);
