@@ -25,10 +25,14 @@
 // shared memory, so nothing is written back, which operands in tensor memory or shared memory would
 // need, and at 8 columns the rate of the instruction is not the bound (0.49 a clock and SM measured:
 // the 302 M weights of 8 experts of 3 x 2048 x 6144 take 4 us).  The columns are the digits of x: x
-// and h are 24-bit fixed point per row, as three signed byte digits (65536 h + 256 m + l), and columns
-// 4 t .. 4 t + 2 hold the middle, low and high digit of the group's token t (two tokens a pass).  All
-// sums of a block (Q8_0, Q4_0) or of a part of the row (int4, int2) are exact integers; the only
-// approximation is |x - s X| <= about 2^-24 max|row|.  Nibble and 2-bit weights are taken as signed
+// and h are 32-bit fixed point per row, as four signed byte digits, and columns 4 t .. 4 t + 3 hold the
+// digits of 256, 1, 2^24 and 65536 of the group's token t (two tokens a pass).  All sums of a block
+// (Q8_0, Q4_0) or of a part of the row (int4, int2) are exact integers; the only approximation is
+// |x - s X| <= 2^-23 |x| + 2^-32 max|row|.  Three digits (2^-24 max|row|) fill the columns no better, and
+// one large value coarsens the whole row: where the weights on it are zero, an outlier of 1e4 costs 4e-4
+// of max|y| with three, 2e-6 with four (three / four digits: 44.9 / 45.6 us at one and 236.5 / 240 us at
+// eight tokens of the 256-expert layer, 92.0 / 93.5 us at five of the 128-expert layer).
+// Nibble and 2-bit weights are taken as signed
 // bytes in place (a nibble in the high half of its byte is 16 q, a 2-bit code in the top bits 64 q;
 // q - 8 of Q4_0 is the two's-complement nibble u ^ 8): no offset corrections.
 //
@@ -61,12 +65,12 @@ constexpr int kMlConsumers = 32 * kMlWarps;
 constexpr int kMlHelpers = 3;                      // warps that select the experts and finish h
 constexpr int kMlThreads = kMlConsumers + 32 + 32 * kMlHelpers;  // + producer warp
 constexpr int kMlSlots = 8;                        // items in the ring
-constexpr int kMlDigitMax = 8355700;               // of 127 * 65793: x * inv rounds up by less than 4
+constexpr int kMlDigitMax = 0x7F7F7000;            // of 127 * 0x1010101: x * inv rounds up by less than 512
 constexpr int kMlBar = 32;                         // words between barrier counters
 constexpr int kMlHmax = 4 * kMlBar;                // the rows' max|h| behind the counters
 
 // ---------------------------------------------------------------- integer form of x and h
-// A row is three planes of bytes (middle, low, high digits) at a pitch of ml_plane(cols).  Byte
+// A row is four planes of bytes (the digits of 256, 1, 2^24, 65536) at a pitch of ml_plane().  Byte
 // order within 32 values, following how a weight word yields its values:
 //   nibbles: word 2m = even, 2m+1 = odd elements of 8m..8m+7;  Q8_0: word 2m = elements 4m..4m+3,
 //   2m+1 = 16+4m..;  int2: word 4w + k = elements 16w + k + 4b, b = 0..3.
@@ -74,18 +78,22 @@ enum MlOrder : int { kMlBytes = 0, kMlNibbles = 1, kMlPairs = 2 };
 __host__ __device__ constexpr int ml_order(int fmt) {
   return fmt == BQG_Q8_0 ? kMlBytes : fmt == BQG_I2_ROW ? kMlPairs : kMlNibbles;
 }
-// 48 mod 128: the three planes' 16-byte (and 8-byte) reads of a warp fall into different banks.
-__host__ __device__ constexpr int ml_plane(int cols) { return cols + (48 - cols % 128 + 128) % 128; }
+// 48 (32) mod 128: the four planes' 16-byte reads of int4 and int2 tiles (8-byte reads of the block formats')
+// in a wavefront fall into different banks.
+__host__ __device__ constexpr int ml_plane(int fmt, int cols) {
+  return cols + ((fmt == BQG_I4_ROW || fmt == BQG_I2_ROW ? 48 : 32) - cols % 128 + 128) % 128;
+}
 
 __device__ __forceinline__ uint32_t ml_pack(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t sel) {
   return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
 }
-// `rows` rows of `cols` fp32 values, row r's max|v| given by its bits in most[r] -> digit rows.  A lane takes four values at a time, i0, i0 + step, ... of all (a warp's lanes
-// are consecutive, and all of them call this); neighbours exchange bytes where a word's values are
-// apart.  Not inlined: x's call brings the code in for h's.
-__device__ __noinline__ void ml_convert(const float* src, int rows, int cols, const uint32_t* most, int order, uint8_t* dst,
-                                        int i0, int step) {
-  const int per = cols / 4, n = rows * per, plane = ml_plane(cols);
+// `rows` rows of `cols` fp32 values, row r's max|v| given by its bits in most[r] -> digit rows.  A lane
+// takes four values at a time, i0, i0 + step, ... of all (a warp's lanes are consecutive, and all of them
+// call this); neighbours exchange bytes where a word's values are apart.  Not inlined: x's call brings the
+// code in for h's.
+__device__ __noinline__ void ml_convert(const float* src, int rows, int cols, const uint32_t* most, int order, int plane,
+                                        uint8_t* dst, int i0, int step) {
+  const int per = cols / 4, n = rows * per;
   const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
 #pragma unroll 1
   for (int i = i0; (i & ~31) < n; i += 4 * step) {
@@ -102,21 +110,23 @@ __device__ __noinline__ void ml_convert(const float* src, int rows, int cols, co
         const int w = c & 7;
         c += (w < 4 ? 2 * w : 2 * w - 7) - w;
       }
-      at[u] = r * 3 * plane + 4 * c;
+      at[u] = r * 4 * plane + 4 * c;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int k = i + u * step;
       if ((k & ~31) >= n) break;
-      const float inv = m[u] > 1e-30f ? float(kMlDigitMax) / m[u] : 0.f;  // below, Inf and NaN: zeros
+      // in two factors, since kMlDigitMax over the smallest maxima is beyond fp32; Inf and NaN: zeros
+      const float raise = m[u] < 0x1p-64f ? 0x1p64f : 1.f;
+      const float inv = m[u] > 0.f ? float(kMlDigitMax) / (m[u] * raise) : 0.f;
       const float f[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
       uint32_t t[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)  // adding 128 to every digit, with carries, and taking it off without
-        t[j] = (uint32_t(__float2int_rn(f[j] * inv)) + 0x808080u) ^ 0x808080u;
+        t[j] = (uint32_t(__float2int_rn(f[j] * raise * inv)) + 0x80808080u) ^ 0x80808080u;
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        const uint32_t sel = p == 0 ? 0x0051u : p == 1 ? 0x0040u : 0x0062u;
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t sel = p == 0 ? 0x0051u : p == 1 ? 0x0040u : p == 2 ? 0x0073u : 0x0062u;
         uint32_t w;
         if (order == kMlNibbles) {  // the even lane takes the pair's even values
           const uint32_t mine = ml_pack(t[0], t[2], t[1], t[3], sel), other = __shfl_xor_sync(0xffffffffu, mine, 1);
@@ -135,7 +145,9 @@ __device__ __noinline__ void ml_convert(const float* src, int rows, int cols, co
     }
   }
 }
-__device__ __forceinline__ float ml_row_scale(uint32_t most) { return __uint_as_float(most) * (1.f / float(kMlDigitMax)); }
+// What a sum of products with digits stands for: times this (and the formats' byte forms), the weights' scales,
+// and the row's max|v| last, so that no factor leaves fp32's range on the way.
+constexpr float kMlDigitUnit = 1.f / float(kMlDigitMax);
 
 template <int V>
 struct MlInt {
@@ -262,13 +274,9 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, in
         step(r[k], x[k], s + k);
       }
     }
-    const float ma = odd ? 65536.f : 256.f, mb = odd ? 0.f : 1.f;
-    out[0] = fmaf(float(c[0][0] + c[1][0]), ma, float(c[0][1] + c[1][1]) * mb);
-    out[1] = fmaf(float(c[0][2] + c[1][2]), ma, float(c[0][3] + c[1][3]) * mb);
+    out[0] = fmaf(float(c[0][0] + c[1][0]), 256.f, float(c[0][1] + c[1][1]));
+    out[1] = fmaf(float(c[0][2] + c[1][2]), 256.f, float(c[0][3] + c[1][3]));
   } else {
-    // 256 m + l of a block in the even lanes.  The odd lanes' second column is the high digit again:
-    // 255 h + h.
-    const int mul = odd ? 255 : 256;
     float acc[2] = {};
     constexpr int kUnit = FMT == BQG_Q8_0 ? 34 : 18;
     a0 += s0 * 2 * kUnit;
@@ -299,9 +307,9 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, in
         ml_mma(c, ((w0 << 4) ^ 0x88888888u) & 0xF0F0F0F0u, ((w1 << 4) ^ 0x88888888u) & 0xF0F0F0F0u,
                (w0 ^ 0x88888888u) & 0xF0F0F0F0u, (w1 ^ 0x88888888u) & 0xF0F0F0F0u, x.x, x.y);
       }
-      // |c| <= 32 * 2^14: 256 of them fit int32
-      acc[0] = fmaf(float(c[0] * mul + c[1]), half_bits_to_float(h0), acc[0]);
-      acc[1] = fmaf(float(c[2] * mul + c[3]), half_bits_to_float(h1), acc[1]);
+      // the lane's two digits; |c| <= 32 * 2^14: 257 of them fit int32
+      acc[0] = fmaf(float(c[0] * 256 + c[1]), half_bits_to_float(h0), acc[0]);
+      acc[1] = fmaf(float(c[2] * 256 + c[3]), half_bits_to_float(h1), acc[1]);
     };
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) load_digits(xs[k]);
@@ -322,9 +330,12 @@ __device__ __forceinline__ void ml_tile(uint32_t a0, uint32_t a1, uint64_t b, in
         }
       }
     }
-    out[0] = acc[0] * (odd ? 256.f : 1.f);
-    out[1] = acc[1] * (odd ? 256.f : 1.f);
+    out[0] = acc[0];
+    out[1] = acc[1];
   }
+  // the odd lanes have the high half of the digits
+  out[0] *= odd ? 65536.f : 1.f;
+  out[1] *= odd ? 65536.f : 1.f;
   out[0] += __shfl_xor_sync(0xffffffffu, out[0], 1);
   out[1] += __shfl_xor_sync(0xffffffffu, out[1], 1);
 }
@@ -345,6 +356,7 @@ struct MlFam {           // matrices of the routed experts (0) or of the shared 
   int parts1, parts2;    // of an item's k range
   int y_first, y_step;   // place of the down sums: [pair][part][rows_cta]
   int x_set;             // which of the digit forms of x it reads
+  int h_plane;           // pitch of a plane of h's digits
 };
 
 struct MlParams {
@@ -362,10 +374,10 @@ struct MlParams {
   uint8_t* xrec[2];      // digit rows in global memory (when they do not fit shared memory)
   uint8_t* hrec[2];
   int x_sets;            // 1 or 2 byte orders of x
-  int set_order[2];
+  int set_order[2], set_plane[2];
   int x_smem, h_smem;    // the digit rows are in shared memory
   // shared memory layout
-  int ring_bytes, rec_off, sum_off, y_off, rows_cta;
+  int ring_bytes, rec_off, sum_off, rows_cta;
   int parts_max;         // most parts of an item of phase 1
 };
 
@@ -545,8 +557,8 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
   const int b = int(blockIdx.x), G = int(gridDim.x);
   const int pairs = P.tokens * P.top_k;
   uint8_t* rec_s = smem + P.rec_off;
-  float* sums = reinterpret_cast<float*>(smem + P.sum_off);    // phase 1: [slot][part][pair of the item][16]
-  float* y_sums = reinterpret_cast<float*>(smem + P.y_off);    // phase 2: [pairs, then tokens][part][rows_cta]
+  float* sums = reinterpret_cast<float*>(smem + P.sum_off);  // phase 1: [slot][part][pair of the item][16]
+  float* y_sums = sums;  // phase 2: [pairs, then tokens][part][rows_cta]; the helpers are through before barrier 2
   const int hr0 = ml_share(P.hidden, b), rows = ml_share(P.hidden, b + 1) - hr0;
   const int n_shared = P.has_shared ? P.fam[1].items : 0;      // phase 1: the shared expert's items come first
 
@@ -742,8 +754,8 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
             gs += in[c * step + k * 16 + f];
             us += in[c * step + k * 16 + 8 + f];
           }
-          const float sx = ml_row_scale(S.xmax[p >> 8]);
-          const float h = act_fn(P.act, gs * sx) * (us * sx);
+          const float xm = __uint_as_float(S.xmax[p >> 8]);
+          const float h = act_fn(P.act, gs * xm) * (us * xm);
           P.h[fam][size_t((p & 255) - fam_pairs) * F.inter + r0 + f] = h;
           most = __float_as_uint(h) & 0x7fffffffu;
         }
@@ -832,10 +844,11 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       }
     }
     // x in integer form: the CTA's own copy, or its share of the copy in global memory
-    const int x_row = 3 * ml_plane(P.hidden);
+    const int set1 = P.tokens * 4 * P.set_plane[0];  // place of the second set of x in shared memory
     const int i0 = tid + (P.x_smem ? 0 : b * kMlConsumers), i_step = P.x_smem ? kMlConsumers : G * kMlConsumers;
     for (int s = 0; s < P.x_sets; ++s)
-      ml_convert(P.x, P.tokens, P.hidden, S.xmax, P.set_order[s], P.x_smem ? rec_s + s * P.tokens * x_row : P.xrec[s], i0, i_step);
+      ml_convert(P.x, P.tokens, P.hidden, S.xmax, P.set_order[s], P.set_plane[s], P.x_smem ? rec_s + s * set1 : P.xrec[s],
+                 i0, i_step);
     ml_consumers_sync();
     if (!P.x_smem && tid == 0) ml_arrive(P.bar);
     if (P.tokens > 1 && warp < P.tokens) {
@@ -882,15 +895,15 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       const int grp = warp / size, unit = warp - grp * size, j = unit % parts, tile = 8 * (unit / parts);
       const int fmt = F.fmt, cols = first ? P.hidden : F.inter, rb = first ? F.rb1 : F.rb2, units = cols / 32;
       const int steps = ml_steps(fmt, cols), s0 = steps * j / parts, s1 = steps * (j + 1) / parts;
-      const int plane = ml_plane(cols);
+      const int plane = first ? P.set_plane[F.x_set] : F.h_plane;
       const bool in_smem = first ? P.x_smem : P.h_smem;
       const uint8_t* recs;
-      if (first) recs = in_smem ? rec_s + F.x_set * P.tokens * x_row : P.xrec[F.x_set];
-      else recs = in_smem ? rec_s + (fam ? pairs * 3 * ml_plane(P.fam[0].inter) : 0) : P.hrec[fam];
-      // the column's plane (column 3 repeats the high digits) and the lane's part of a step
+      if (first) recs = in_smem ? rec_s + F.x_set * set1 : P.xrec[F.x_set];
+      else recs = in_smem ? rec_s + (fam ? pairs * 4 * P.fam[0].h_plane : 0) : P.hrec[fam];
+      // the column's plane and the lane's part of a step
       const uint64_t rec0 = (in_smem ? uint64_t(smem_u32(recs)) : reinterpret_cast<uint64_t>(recs)) +
-                            uint32_t(min(g & 3, 2) * plane + (ml_rowwise(fmt) ? 32 : 8) * q);
-      const float form = fmt == BQG_Q8_0 ? 1.f : fmt == BQG_I2_ROW ? 1.f / 64.f : 1.f / 16.f;
+                            uint32_t((g & 3) * plane + (ml_rowwise(fmt) ? 32 : 8) * q);
+      const float form = kMlDigitUnit * (fmt == BQG_Q8_0 ? 1.f : fmt == BQG_I2_ROW ? 1.f / 64.f : 1.f / 16.f);
       const int fam_pairs = fam ? pairs : 0;
       // `done` counts all the warps: the groups' number for each of the item's warps, the first one the rest
       const int count = groups + (unit == 0 ? kMlWarps - size * groups : 0);
@@ -921,7 +934,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         for (int k = 0; k < np; k += 2) {
           // the column's pair (past the item's last: that one again)
           const int p = S.order[d.z + min(k + (g >> 2), np - 1)];
-          const uint64_t bb = rec0 + uint32_t((first ? p >> 8 : (p & 255) - fam_pairs) * 3 * plane);
+          const uint64_t bb = rec0 + uint32_t((first ? p >> 8 : (p & 255) - fam_pairs) * 4 * plane);
           float v[2];
           auto run = [&](auto fmt_c) {
             if (in_smem) ml_tile<decltype(fmt_c)::value, true>(a0, a1, bb, units, s0, s1, v);
@@ -935,7 +948,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
           }
           const int kk = k + (q >> 1);
           if (!(q & 1) && kk < np) {
-            const float y0 = (g & 1 ? v[1] : v[0]) * (rs0 * form), y1 = (g & 1 ? v[0] : v[1]) * (rs1 * form);
+            const float y0 = (g & 1 ? v[1] : v[0]) * form * rs0, y1 = (g & 1 ? v[0] : v[1]) * form * rs1;
             if (first) {
               float* out = sums + ((slot * P.parts_max + j) * P.tokens + kk) * 16 + g;
               out[0] = y0;
@@ -972,7 +985,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         const int c0 = tid + (P.h_smem ? 0 : b * kMlConsumers), step = P.h_smem ? kMlConsumers : G * kMlConsumers;
         for (int f = 0; f <= P.has_shared; ++f)
           ml_convert(P.h[f], f ? P.tokens : pairs, P.fam[f].inter, S.hmax + (f ? pairs : 0), ml_order(P.fam[f].fmt),
-                     P.h_smem ? rec_s + (f ? pairs * 3 * ml_plane(P.fam[0].inter) : 0) : P.hrec[f], c0, step);
+                     P.fam[f].h_plane, P.h_smem ? rec_s + (f ? pairs * 4 * P.fam[0].h_plane : 0) : P.hrec[f], c0, step);
       }
       ml_consumers_sync();
       if (!P.h_smem) {
@@ -996,7 +1009,7 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
         float v = 0.f;
 #pragma unroll 2
         for (int c = 0; c < F.parts2; ++c) v += at[c * P.rows_cta];
-        at[0] = v * ml_row_scale(S.hmax[p]) * (fam ? 1.f : S.sel_w[p]);
+        at[0] = v * __uint_as_float(S.hmax[p]) * (fam ? 1.f : S.sel_w[p]);
       }
     }
     ml_consumers_sync();
@@ -1024,7 +1037,12 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
 // ---------------------------------------------------------------- host side
 static_assert((kMlHmax + kMlMaxPairs + kMlMaxTokens) * sizeof(uint32_t) <= BQG_MOE_LAYER_STATE_BYTES, "barriers and max|h|");
 
-constexpr size_t kMlXCap = 100 * 1024;   // digit rows kept in shared memory (the ring needs the rest)
+// Digit rows kept in shared memory; the ring needs the rest, and digits from L2 cost less than small items.
+// us at these caps / with x's at 133 KB / with h's at 107 KB: 5 tokens of the 128-expert layer 93.5 / 93.5 /
+// 93.5 (x's at 100 KB: 95.7), 5 tokens of the 256-expert int4 layer 161 / 229 / 161 and int2 149 / 146 / 149,
+// 8 tokens of 32 Q8_0 experts of 7168 x 4096 770 / 1232 / 770, 4 tokens of 64 Q4_0 experts of 1536 x 4096 82 /
+// 82 / 106, of 64 Q8_0 experts of 704 x 2816 67 / 67 / 84.
+constexpr size_t kMlXCap = 120 * 1024;
 constexpr size_t kMlHCap = 80 * 1024;
 constexpr size_t kMlSmem = 227 * 1024 - sizeof(MlShared) - 1024;
 // Most bytes of an item.  An item's tile takes the same MMAs however few its rows: with 28 KB the
@@ -1033,7 +1051,7 @@ constexpr int kMlItem = 56 * 1024;
 
 struct MlLayout {
   size_t bar, logits, h[2], xrec[2], hrec[2], total;
-  int x_sets, set_order[2], x_set[2], x_smem, h_smem;
+  int x_sets, set_order[2], set_plane[2], x_set[2], h_plane[2], x_smem, h_smem;
   size_t rec_bytes;
 };
 
@@ -1052,32 +1070,37 @@ inline MlLayout ml_layout(const bqg_moe_layer* L, int tokens) {
   o.h[0] = take(4 * pairs * L->inter);
   o.h[1] = sh ? take(4 * T * L->shared_inter) : 0;
   o.set_order[0] = ml_order(L->expert_fmt);
+  o.set_plane[0] = ml_plane(L->expert_fmt, L->hidden);
+  o.h_plane[0] = ml_plane(L->expert_fmt, L->inter);
+  o.h_plane[1] = sh ? ml_plane(L->shared_fmt, L->shared_inter) : 0;
   o.x_sets = 1;
   if (sh && ml_order(L->shared_fmt) != o.set_order[0]) {
     o.x_set[1] = 1;
     o.set_order[1] = ml_order(L->shared_fmt);
+    o.set_plane[1] = ml_plane(L->shared_fmt, L->hidden);
     o.x_sets = 2;
   }
-  // 640 bytes more: the last step of a row may read past its last unit, and the loads run two ahead
-  const size_t xb = T * 3 * ml_plane(L->hidden);
-  const size_t hb0 = pairs * 3 * ml_plane(L->inter), hb1 = sh ? T * 3 * ml_plane(L->shared_inter) : 0;
-  o.x_smem = xb * o.x_sets <= kMlXCap;
+  // 640 bytes more in global memory: the last step of a row may read past its last unit, and the loads run
+  // two ahead (in shared memory it reads the sums, which are more than that)
+  const size_t xb[2] = {T * 4 * o.set_plane[0], T * 4 * o.set_plane[1]};
+  const size_t hb0 = pairs * 4 * o.h_plane[0], hb1 = T * 4 * o.h_plane[1];
+  o.x_smem = xb[0] + xb[1] <= kMlXCap;
   o.h_smem = hb0 + hb1 <= kMlHCap;
   if (!o.x_smem)
-    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb + 640);
+    for (int s = 0; s < o.x_sets; ++s) o.xrec[s] = take(xb[s] + 640);
   if (!o.h_smem) {
     o.hrec[0] = take(hb0 + 640);
     o.hrec[1] = sh ? take(hb1 + 640) : 0;
   }
-  if (o.x_smem) o.rec_bytes = xb * o.x_sets;
+  if (o.x_smem) o.rec_bytes = xb[0] + xb[1];
   if (o.h_smem && hb0 + hb1 > o.rec_bytes) o.rec_bytes = hb0 + hb1;
-  o.rec_bytes = (o.rec_bytes + 640 + 127) / 128 * 128;
+  o.rec_bytes = (o.rec_bytes + 127) / 128 * 128;
   o.total = off;
   return o;
 }
 
 inline MlFam ml_fam(int fmt, int hidden, int inter, const void* gate, const void* up, const void* down, size_t gs,
-                    size_t us, size_t ds, int x_set, int grid, int most) {
+                    size_t us, size_t ds, int x_set, int h_plane, int grid, int most) {
   MlFam F{};
   F.gate = static_cast<const uint8_t*>(gate);
   F.up = static_cast<const uint8_t*>(up);
@@ -1107,6 +1130,7 @@ inline MlFam ml_fam(int fmt, int hidden, int inter, const void* gate, const void
   F.tiles = ((F.nr + 1) / 2 + 7) / 8;
   F.second2 = place((F.nr + 1) / 2 * F.rb2);
   F.x_set = x_set;
+  F.h_plane = h_plane;
   return F;
 }
 
@@ -1120,6 +1144,7 @@ inline int ml_parts(int fmt, int cols, int tiles, int items_cta, int passes, int
   return best;
 }
 
+static_assert(kMlSlots * 4 * 64 >= 640, "the sums behind the digit rows");
 inline SmemAttrOnce g_ml_attr;
 
 }  // namespace bqg
@@ -1159,16 +1184,17 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   const int parts2_max[2] = {tokens <= 2 ? 8 : tokens <= 4 ? 4 : 2, 8};
   const size_t sum_bytes = size_t(kMlSlots) * P.parts_max * tokens * 64;
   const size_t y_bytes = (size_t(pairs * parts2_max[0] + (sh ? tokens * parts2_max[1] : 0)) * P.rows_cta * 4 + 127) / 128 * 128;
-  P.ring_bytes = int((kMlSmem - lay.rec_bytes - sum_bytes - y_bytes) / 128 * 128);
+  const size_t sums = sum_bytes > y_bytes ? sum_bytes : y_bytes;  // of either phase, one after the other
+  P.ring_bytes = int((kMlSmem - lay.rec_bytes - sums) / 128 * 128);
   P.rec_off = P.ring_bytes;
   P.sum_off = P.rec_off + int(lay.rec_bytes);
-  P.y_off = P.sum_off + int(sum_bytes);
-  const size_t smem = size_t(P.y_off) + y_bytes;
+  const size_t smem = size_t(P.sum_off) + sums;
   // at least three items in the ring
   const int most = P.ring_bytes / 3 - 256 < kMlItem ? P.ring_bytes / 3 - 256 : kMlItem;
   P.fam[0] = ml_fam(L->expert_fmt, L->hidden, L->inter, L->gate, L->up, L->down, L->gate_stride, L->up_stride,
-                    L->down_stride, 0, kMlGrid, most);
-  P.fam[1] = sh ? ml_fam(L->shared_fmt, L->hidden, L->shared_inter, L->s_gate, L->s_up, L->s_down, 0, 0, 0, lay.x_set[1], kMlGrid, most)
+                    L->down_stride, 0, lay.h_plane[0], kMlGrid, most);
+  P.fam[1] = sh ? ml_fam(L->shared_fmt, L->hidden, L->shared_inter, L->s_gate, L->s_up, L->s_down, 0, 0, 0, lay.x_set[1],
+                         lay.h_plane[1], kMlGrid, most)
                 : P.fam[0];
   auto up = [](int a, int b) { return (a + b - 1) / b; };
   const int items1 = up((sh ? P.fam[1].items : 0) + touched * P.fam[0].items, kMlGrid);
@@ -1199,6 +1225,7 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
     P.xrec[i] = ws + lay.xrec[i];
     P.hrec[i] = ws + lay.hrec[i];
     P.set_order[i] = lay.set_order[i];
+    P.set_plane[i] = lay.set_plane[i];
   }
   P.x_sets = lay.x_sets;
   P.x_smem = lay.x_smem;

@@ -317,8 +317,11 @@ BQG_API int moe_forward(const bqg_moe_layer* L, const float* x, const int32_t* i
  *              first BQG_MOE_LAYER_STATE_BYTES once before the first call (cudaMemset); every call leaves
  *              them zero again, also one that set BQG_DEVERR_TIMEOUT.  The rest is scratch.  Calls
  *              that share a workspace must be ordered (one stream, or graphs replayed in order).
- *   x and h are held as 24-bit fixed point per row (|v - s V| <= about 2^-24 max|row|), so y is as
- *   exact as fp32 sums are, relative to max|y|; a row whose max|v| is below 1e-30 counts as zeros; logits and weights are fp32.  Deterministic.  The kernel is a
+ *   x and h are held as 32-bit fixed point per row (|v - s V| <= 2^-23 |v| + 2^-32 max|row|); sums of
+ *   a block or of a part of a row are exact integers, all else is fp32.  y is therefore as exact as
+ *   fp32 sums are, plus at most 2^-32 max|row| sum_i |W_i| in each product: within 1e-5 of max|y|
+ *   unless a value some 1e4 times its row's root mean square meets weights next to zero, where the
+ *   error grows with that value.  Logits and weights are fp32.  Deterministic.  The kernel is a
  *   cooperative launch of one CTA per SM: it starts when every SM can take its CTA. */
 #define BQG_MOE_LAYER_STATE_BYTES 1024
 BQG_API size_t moe_layer_workspace_size(const bqg_moe_layer* L, int tokens);
