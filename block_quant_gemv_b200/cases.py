@@ -3,12 +3,18 @@
     python -m block_quant_gemv_b200.cases decode  [--layers 22] [--argmax] [--iters 5]
     python -m block_quant_gemv_b200.cases prefill [--tokens 128] [--n 14336] [--k 4096] [--iters 5]
     python -m block_quant_gemv_b200.cases moe gemma|glm [--tokens 1] [--experts E] [--path P] [--iters 5]
+    python -m block_quant_gemv_b200.cases layer gemma|glm [--tokens 1] [--experts E] [--iters 5]
+    python -m block_quant_gemv_b200.cases rows [--tokens 8192] [--k 4096] [--pad 0] [--type bf16] [--iters 5]
+    python -m block_quant_gemv_b200.cases product [--tokens 8192] [--k 4096] [--n 14336] [--type bf16] [--iters 5]
 
 decode:  one TinyLlama-shape decode step (7 Q4_0 projections per layer + the Q8_0 LM head),
          all matrices in one qgemv_batched launch per call.
 prefill: qgemm_prefill of a Q4_0 [n x k] matrix with fp16 X [tokens x k].
 moe:     one routed-expert layer: (router logits for the Gemma-like layer,) top-k routing
          and moe_forward; the GLM-like layer takes N(0,1) logits.
+layer:   moe_layer, the same layers' router and experts in one kernel.
+rows:    quantize_rows_i8 of [tokens x k] values, --pad more values from one row to the next.
+product: qgemm_i8 of int8 [tokens x k] and [n x k].
 Inputs are the seeded synthetic tensors of the benchmark (seed 0).  Prints the mean time per
 call (CUDA events, after two warm-up calls) and the device error bits.
 """
@@ -81,14 +87,42 @@ def moe(args) -> str:
     w = torch.empty(tok, spec.top_k, device="cuda")
     y = torch.empty(tok, spec.hidden, device="cuda")
     ws = torch.empty(bqg.moe_workspace_size(L, tok), dtype=torch.uint8, device="cuda")
+    if args.case == "layer":
+        R = synth.normal_f32(0, synth.stream_id("layer/R"), spec.n_experts * spec.hidden, std=0.02)
+        R, whole = R.view(spec.n_experts, spec.hidden).cuda(), bqg.moe_layer_workspace(L, tok)
 
     def step():
+        if args.case == "layer":
+            bqg.moe_layer(L, R, x, y, idx, w, whole)
+            return
         if spec.router:
             bqg.moe_router_logits(T.R, x, logits)
         bqg.moe_router_topk(logits, spec.top_k, idx, w)
         bqg.moe_forward(L, x, idx, w, y, ws)
     us = _time(step, args.iters)
-    return f"moe {spec.name} T={tok}: {us:.1f} us per layer (router included)"
+    return f"{args.case} {spec.name} T={tok}: {us:.1f} us per layer (router included)"
+
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def rows(args) -> str:
+    t, k, dtype = args.tokens, args.k, TYPES[args.type]
+    X = torch.empty(t, k + args.pad, dtype=dtype, device="cuda")[:, :k]
+    X.copy_(synth.normal_f32(0, synth.stream_id("rows/X"), t * k).view(t, k))
+    Xq, scale = bqg.quantize_rows_i8(X)
+    us = _time(lambda: bqg.quantize_rows_i8(X, Xq, scale), args.iters)
+    moved = t * k * (X.element_size() + 1) + 4 * t
+    return f"rows {t}x{k} {args.type} pitch {k + args.pad}: {us:.1f} us per call, {moved / us / 1e6:.2f} TB/s"
+
+
+def product(args) -> str:
+    t, n, k = args.tokens, args.n, args.k
+    Xq, sx = bqg.quantize_rows_i8(synth.normal_f32(0, synth.stream_id("product/X"), t * k).view(t, k).cuda())
+    Wq, sw = bqg.quantize_rows_i8(synth.normal_f32(0, synth.stream_id("product/W"), n * k).view(n, k).cuda())
+    Y = torch.empty(t, n, dtype=TYPES[args.type], device="cuda")
+    us = _time(lambda: bqg.qgemm_i8(Xq, sx, Wq, sw, Y=Y), args.iters)
+    return f"product {t}x{k}x{n} {args.type}: {us:.1f} us per call, {2.0 * t * n * k / us / 1e9:.2f} POP/s"
 
 
 def main(argv=None):
@@ -101,18 +135,27 @@ def main(argv=None):
     p.add_argument("--tokens", type=int, default=128)
     p.add_argument("--n", type=int, default=14336)
     p.add_argument("--k", type=int, default=4096)
-    m = sub.add_parser("moe")
-    m.add_argument("layer", choices=["gemma", "glm"])
-    m.add_argument("--tokens", type=int, default=1)
-    m.add_argument("--experts", type=int, default=0, help="routed experts (default: the layer's own count)")
+    m, w = sub.add_parser("moe"), sub.add_parser("layer")
+    for s in (m, w):
+        s.add_argument("layer", choices=["gemma", "glm"])
+        s.add_argument("--tokens", type=int, default=1)
+        s.add_argument("--experts", type=int, default=0, help="routed experts (default: the layer's own count)")
     m.add_argument("--path", type=int, default=0, help="0 automatic, 1 CUDA cores, 2 tensor cores")
-    for s in (d, p, m):
+    w.set_defaults(path=0)
+    r, q = sub.add_parser("rows"), sub.add_parser("product")
+    for s in (r, q):
+        s.add_argument("--tokens", type=int, default=8192)
+        s.add_argument("--k", type=int, default=4096)
+        s.add_argument("--type", choices=list(TYPES), default="bf16", help="of the rows; of the product's output")
+    r.add_argument("--pad", type=int, default=0)
+    q.add_argument("--n", type=int, default=14336)
+    for s in (d, p, m, w, r, q):
         s.add_argument("--iters", type=int, default=5)
     args = ap.parse_args(argv)
     assert torch.cuda.is_available(), "needs a CUDA device"
     torch.cuda.set_device(0)
     bqg.lib()
-    msg = {"decode": decode, "prefill": prefill, "moe": moe}[args.case](args)
+    msg = {"decode": decode, "prefill": prefill, "moe": moe, "layer": moe, "rows": rows, "product": product}[args.case](args)
     torch.cuda.synchronize()
     print(msg)
     print("device errors:", bqg.bqg_device_errors())
