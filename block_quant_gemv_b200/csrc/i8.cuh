@@ -108,8 +108,9 @@ struct Elem<__nv_bfloat16> {
 // to kQrChunks chunks of 8 values in registers, so rows of up to TPR * 32 values are read once; longer
 // rows read the rest a second time (from L2).  Bytes bound it: 1 read and 1 write of the row; of the
 // TPR that hold a row, the smallest has the most bytes in flight (8192 x 4096 bf16: 128 threads a row
-// 22.2 us; 256, and every rounding decided the long way, 40 us), the largest the shortest way for few
-// rows.  fp32 rows of 4096: 27.1 us, 6.2 TB/s.
+// 21.9 us, bound by instructions: 3.0 of 4 issue slots a clock; 256, and every rounding decided the long
+// way, 40 us), the largest the shortest way for few rows.  fp32 rows of 4096: 27.3 us, 6.1 TB/s.  VEC false
+// (rows off 16 bytes, read value by value): 30.4 and 38.6 us.
 //
 // The rounding is decided exactly.  t = x * (1 / s) + 1.5 * 2^23 is rounded once, to a whole number
 // n (in t's low bits); x * (1 / s) is off from x / s by less than 127 * 2^-24 * 1.1, so wherever it
@@ -429,7 +430,7 @@ __device__ __forceinline__ bool it_all_go_on(bool ok) {
 
 // SPLIT: where the tiles would leave SMs idle, a cluster of CTAs takes one tile, each a part of k; they
 // exchange their int32 sums through shared memory, each adding and storing its share of the tokens.
-// 24 x 4096 x 4096: 11.0 us on 32 SMs, 7.2 us on 128; 30 x 8192 x 1000: 19.4 and 7.6 us.
+// 24 x 4096 x 4096: 11.0 us on 32 SMs, 7.4 us on 128; 30 x 8192 x 1000: 19.4 and 7.6 us.
 template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kItThreads, 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kItThreads, 1)
 // 128 k for the same MMAs that take 48 KB as a 128 x 256 tile of its own, whose 94 bytes a clock are
 // more than an SM gets from L2.  The warps' parts are k_i8_gemm's, but eight warps store.
 // 8192 tokens, k 4096, n 14336, bf16 out: 457 us as 128 x 256 tiles (2.1 POP/s), 435 us with four storing
-// warps (a tile's 256 columns took longer than its 32 stages), 308 us (3.1 POP/s; tensor pipe 82 % active).
+// warps (a tile's 256 columns took longer than its 32 stages), 322 us (3.0 POP/s; tensor pipe 87 % active).
 constexpr int kI2Half = 128;
 constexpr int kI2Threads = 320;  // 8 warps store: a quarter of the channels and half of the tokens each
 constexpr int kI2StageBytes = 2 * kI2Half * kItK;

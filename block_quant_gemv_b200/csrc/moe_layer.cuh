@@ -42,12 +42,11 @@
 // added in order afterwards, so results do not depend on timing.
 //
 // Measured (us a call; weights' bytes at the HBM copy rate in brackets): 128 Q4_0 experts of 704 x 2816,
-// top 8, a shared Q8_0 expert of 2112: one token 34 [7], 5 tokens 92 [21]; 256 int4 experts of 2048 x
-// 6144, top 8: one token 44 [24], 8 tokens 235 [166].  One token: 18 us of the 44 (13 of a layer of 16
-// experts of 256 x 512, 15.5) remain with no items at all: launch, router, two grid barriers, h's way
-// through L2; with almost no MMAs it takes 42.  8 tokens: the digits' way
-// from L2 and the consumers.
-// dp4a, one per digit, in place of the MMA: 77 us and 410 us (256 experts, 1 and 8 tokens).
+// top 8, a shared Q8_0 expert of 2112: one token 35 [7], 5 tokens 93 [21]; 256 int4 experts of 2048 x
+// 6144, top 8: one token 46 [24], 8 tokens 241 [166].  One token: 18 us of the 46 (13 of a layer of 16
+// experts of 256 x 512, 15.8) remain with no items at all: launch, router, two grid barriers, h's way
+// through L2; with almost no MMAs it takes 2 us less.  8 tokens: the digits' way from L2 and the consumers.
+// dp4a, one per digit (of three), in place of the MMA: 77 us and 410 us (256 experts, 1 and 8 tokens).
 #pragma once
 
 #include "common.cuh"
@@ -1177,10 +1176,15 @@ extern "C" int moe_layer(const bqg_moe_layer* L, const float* R, const float* x,
   MlParams P{};
   P.rows_cta = (L->hidden + kMlGrid - 1) / kMlGrid;
   // The sums of a part take 64 bytes a token.  x's digits in global memory: more parts an item, so that
-  // fewer items' tokens share L1 (256-expert layer, 8 tokens: 265 us with 4 parts, 235 us with 6).
+  // fewer items' tokens share L1.  us with about half the parts / these / about twice: 128-expert layer, 2
+  // tokens 50 / 50 / 52, 3 tokens 65 / 65 / 70, 5 tokens 104 / 93 / 97; 256-expert int4 layer, one token 45.6
+  // three times, 6 tokens 196 / 188 / 187, 8 tokens 250 / 240 / 247 (int2: 194 / 216 / 216).
   P.parts_max = tokens <= 2 ? 12 : tokens <= 4 ? 8 : lay.x_smem ? 4 : 6;
-  // of phase 2: routed experts (rows of all pairs) and the shared one, whose item all warps share, since
-  // the ring frees its items in order (5 tokens of the 128-expert layer with 2 parts: 96 us)
+  // of phase 2: routed experts (rows of all pairs), whose sums take the place of the ring, and the shared one,
+  // whose item all warps share, since the ring frees its items in order.  Half / these / twice of the routed
+  // ones': 128-expert layer, 5 tokens 93 / 93 / 104; 256-expert int4 layer, one token 45.5 / 45.6 / 55.8, 8
+  // tokens 244 / 240 / 247; 32 Q8_0 experts of 7168 x 4096, 8 tokens 962 / 769 / 722.  4 of the shared one's:
+  // 8 tokens of the 128-expert layer 132 instead of 130.5.
   const int parts2_max[2] = {tokens <= 2 ? 8 : tokens <= 4 ? 4 : 2, 8};
   const size_t sum_bytes = size_t(kMlSlots) * P.parts_max * tokens * 64;
   const size_t y_bytes = (size_t(pairs * parts2_max[0] + (sh ? tokens * parts2_max[1] : 0)) * P.rows_cta * 4 + 127) / 128 * 128;
