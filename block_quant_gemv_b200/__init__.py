@@ -7,8 +7,8 @@ fallback: if the library is not built, every call raises.
 The functions mirror the C ABI in include/bqg.h (same names):
     qgemv, qgemv_batched, qgemv_argmax, qgemv_batched_argmax (GemvBatch.run(argmax=...)),
     qgemm_prefill, quantize_rows_i8, qgemm_i8, moe_router_logits, moe_router_topk,
-    moe_workspace_size, moe_forward, moe_forward_noalloc, moe_layer_workspace_size, moe_layer, bqg_status_string, bqg_weight_bytes,
-    bqg_device_errors, bqg_selftest_wait_timeout
+    moe_workspace_size, moe_forward, moe_forward_noalloc, moe_layer_workspace_size, moe_layer,
+    bqg_status_string, bqg_weight_bytes, bqg_device_errors, bqg_selftest_wait_timeout
 """
 from __future__ import annotations
 
@@ -549,7 +549,7 @@ def moe_layer(layer: MoELayer, R: torch.Tensor, x: torch.Tensor, y: Optional[tor
         workspace = moe_layer_workspace(layer, tokens, x.device)
     if workspace is not None:
         _need_cuda("workspace", workspace, torch.uint8)
-    _call_on(lib().moe_layer, "moe_layer", (x, R, y, idx, w, workspace, layer.tensors[0]), ctypes.addressof(layer.c),
+    _call_on(lib().moe_layer, "moe_layer", (x, R, y, idx, w, workspace, *layer.tensors), ctypes.addressof(layer.c),
              R.data_ptr(), x.data_ptr(), _vector("y", y, tokens * hidden), idx.data_ptr(), _vector("w", w, tokens * k),
              tokens, 0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return y, idx, w
