@@ -512,9 +512,9 @@ __global__ void __launch_bounds__(kItThreads, 1)
           tma_load_2d(b_ring + size_t(st) * kBBytes, &tmap_x, kk * kItK, tt * BN, &full[st]);
         }
       }
-      if (!ok)  // bounded wait for the copies already issued, so none lands after the CTA exits
-        for (long long q = (s > kStages ? s - kStages : 0); q < s; ++q)
-          mbar_wait(&full[q % kStages], uint32_t(q / kStages) & 1u);
+      // bounded wait for the last copies, so that none lands after the CTA has gone, whoever gave up
+      for (long long q = (s > kStages ? s - kStages : 0); q < s; ++q)
+        mbar_wait(&full[q % kStages], uint32_t(q / kStages) & 1u);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -735,7 +735,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI2Threads, 1)
           tma_load_2d_pair(b_ring + st * kI2Half * kItK, &tmap_x, kk * kItK, tt * kI2N + rank * kI2Half, bar);
         }
       }
-      if (!ok && rank == 0)  // bounded wait for the copies already issued, so none lands after the pair exits
+      if (rank == 0)  // bounded wait for the last copies, so that none lands after the pair has gone, whoever gave up
         for (long long q = (s > kI2Stages ? s - kI2Stages : 0); q < s; ++q)
           mbar_wait(&full[q % kI2Stages], uint32_t(q / kI2Stages) & 1u);
     }

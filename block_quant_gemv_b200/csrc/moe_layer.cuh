@@ -674,10 +674,9 @@ __global__ void __launch_bounds__(kMlThreads, 1) k_moe_layer(const __grid_consta
       }
     }
     if (!listed) ml_list_sync();
-    if (!ok) {  // a bounded wait gave up: wait (bounded) for the copies in flight
-      if (lane == 0) *(volatile int*)&S.abort = 1;
-      for (int k = tail; k < i; ++k) mbar_wait(&S.full[k % kMlSlots], uint32_t(k / kMlSlots) & 1u);
-    }
+    if (!ok && lane == 0) *(volatile int*)&S.abort = 1;
+    // bounded wait for the last copies, so that none lands after the CTA has gone, whoever gave up
+    for (int k = tail; k < i; ++k) mbar_wait(&S.full[k % kMlSlots], uint32_t(k / kMlSlots) & 1u);
   } else if (warp > kMlWarps) {
     // ------------------------------------------------ helpers
     // The first one: selection of one token, and the lists.

@@ -28,17 +28,26 @@ def closing(text, at, pair):
     raise AssertionError("no closing bracket")
 
 
+HEAD = re.compile(r"(?:if|while|for) (?:constexpr )?\(")
+
+
+def statement(text, at):
+    """The statement that starts at or behind `at`, as (start, end)."""
+    start = at + len(text[at:]) - len(text[at:].lstrip())
+    if text[start] == "{":
+        return start, closing(text, start, "{}")
+    head = HEAD.match(text, start)
+    if head:
+        return start, statement(text, closing(text, head.end() - 1, "()"))[1]
+    return start, text.index(";", start)
+
+
 def branches(text):
-    """(condition, body) of every `if` and `while` and the condition of every `for`."""
-    for m in re.finditer(r"\b(?:if|while|for) (?:constexpr )?\(", text):
+    """(condition, body) of every `if`, `while` and `for`."""
+    for m in re.finditer(r"\b" + HEAD.pattern, text):
         end = closing(text, m.end() - 1, "()")
-        cond = text[m.end():end - 1]
-        rest = text[end:].lstrip()
-        start = len(text) - len(rest) if rest else end
-        if text[start] == "{":
-            yield cond, text[start:closing(text, start, "{}")]
-        else:
-            yield cond, text[start:text.index(";", start)]
+        start, stop = statement(text, end)
+        yield text[m.end():end - 1], text[start:stop]
 
 
 def single_thread(cond):
@@ -96,3 +105,15 @@ def test_no_wait_lasts_as_long_as_the_product():
     assert kernel.count("mbar_wait(done") == 1
     wait = kernel.index("mbar_wait(done")
     assert kernel.index("it_store_tile(") < kernel.rindex("__syncthreads()", 0, wait) < wait
+
+
+@pytest.mark.parametrize("name,drain,kernels", [("i8.cuh", r"mbar_wait\(&full\[q %", 2),
+                                                ("moe_layer.cuh", r"mbar_wait\(&S\.full\[k %", 1)])
+def test_copies_in_flight_are_waited_for_whoever_gave_up(name, drain, kernels):
+    """The copying thread waits for its last copies in every case: the warps that use them may have given up
+    without it."""
+    text = source(name)
+    assert len(re.findall(drain, text)) == kernels
+    for cond, body in branches(text):
+        if re.search(r"\bok\b|abort", cond) and ";" not in cond:
+            assert not re.search(drain, body), cond
