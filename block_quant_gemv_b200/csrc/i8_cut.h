@@ -56,8 +56,8 @@ inline I8Cut i8_cut(int tokens, int n, int k, int sms, I8Clusters clusters) {
 // by byte in one lane, and a CTA 32 channels.  Measured, dp4a / tensor cores, us (tokens x k x n):
 //   1, 2 tokens  1 x 512 x 512 1.5 / 3.4, 2 x 1024 x 1024 2.3 / 4.5, 2 x 2048 x 1024 4.6 / 4.9, 1 x 2048 x 14336
 //                7.2 / 8.8; but 1 x 4096 x 1024 8.3 / 5.9, 1 x 4096 x 4096 9.0 / 7.4, 2 x 8192 x 1024 14.3 / 8.1,
-//                unless every SM has a CTA: 1 x 4096 x 4736 8.9 / 12.6, 1 x 4096 x 14336 11.8 / 13.1, 2 x 8192
-//                x 28672 39.0 / 45.1 (against it: 1 x 8192 x 8192 16.8 / 15.1)
+//                unless every SM has a CTA: 1 x 4096 x 5120 9.1 / 9.2, 1 x 4096 x 14336 11.8 / 13.1, 2 x 8192
+//                x 28672 39.0 / 45.1 (against it: 1 x 8192 x 6144 15.6 / 13.6)
 //   odd rows     1 x 500 x 300 2.5 / 3.4, 1 x 4104 x 14336 13.0 / 14.6; but 1 x 4090 x 14336 14.2 / 13.0, 1 x
 //                1023 x 2048 6.0 / 5.0, 1 x 8191 x 256 16.7 / 7.7
 //   3, 4 tokens  4 x 512 x 512 2.2 / 3.4, 4 x 1536 x 1536 4.7 / 6.1, 3 x 2048 x 256 3.9 / 4.3; but 4 x 500 x 300
